@@ -8,7 +8,7 @@ plus its workspace.  PyTorch is used only for device memory and streams.
 
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional
 
 from .binding import (  # noqa: F401  (re-exported C ABI names)
     ENGRAM_BF16, ENGRAM_F32, ENGRAM_FP8, ENGRAM_ERR_CANON, ENGRAM_ERR_INDEX, ENGRAM_ERR_TIMEOUT, ENGRAM_ERR_TOKEN,
@@ -25,8 +25,34 @@ from .binding import (  # noqa: F401  (re-exported C ABI names)
     engram_forward_multibranch, ENGRAM_MAX_BRANCHES, engram_table_grad_workspace_bytes, engram_table_grad,
     engram_table_sgd, engram_host_tier_map, engram_grad_route_workspace_bytes, engram_grad_route,
     engram_grad_combine_workspace_bytes, engram_grad_combine, engram_shard_sgd,
+    engram_embed, engram_embed_grad_workspace_bytes, engram_embed_grad, engram_add_norm,
+    engram_add_norm_grad_workspace_bytes, engram_add_norm_grad,
     engram_last_error, engram_profile_enable, engram_profile_read, engram_project, engram_remap, engram_strerror,
     engram_workspace_bytes, make_config)
+
+
+def _on_stream(stream):
+    """Context in which tensors are allocated for work on `stream` (a torch
+    stream, a raw handle, or None: the current stream), so that the caching
+    allocator hands their memory on only in that stream's order."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+class NormOut(NamedTuple):
+    """Outputs of :meth:`Engram.add_norm`; those not asked for are None."""
+
+    sum: Optional[object]
+    y: Optional[object]
+    q: Optional[object]
+    q_scale: Optional[object]
+    rstd: Optional[object]
 
 
 class Engram:
@@ -163,6 +189,119 @@ class Engram:
     def shard_sgd(self, n_shards: int, shard: int, rows, grad, n_unique, shard_table, lr: float, stream=None):
         """shard_table[row - first] -= lr * grad for the listed global rows."""
         engram_shard_sgd(self.ctx, n_shards, shard, rows, grad, n_unique, rows.shape[0], shard_table, lr, stream)
+
+    # ---- the residual stream around the module
+
+    @property
+    def dtype(self):
+        """torch dtype of the hidden states (h, Y)"""
+        import torch
+        return torch.float32 if self.cfg.dtype == ENGRAM_F32 else torch.bfloat16
+
+    def _want(self, name: str, t, shape, dtype):
+        """Refuse a tensor of another device, dtype or shape, or with gaps."""
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the context on {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} is {t.dtype}, needs {dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    def _want_tokens(self, tok, t_begin: int):
+        """(B, T, row stride) of a token tensor whose rows may be wider than T."""
+        import torch
+        if tok.dim() != 2:
+            raise ValueError(f"tok has {tok.dim()} dimensions, needs 2")
+        if tok.device != self.device:
+            raise ValueError(f"tok is on {tok.device}, the context on {self.device}")
+        if tok.dtype != torch.int32:
+            raise ValueError(f"tok is {tok.dtype}, needs torch.int32")
+        B, T = tok.shape
+        if T > 1 and tok.stride(1) != 1:
+            raise ValueError("the ids of a sequence must be adjacent in memory")
+        if not 0 <= t_begin <= T:
+            raise ValueError(f"t_begin = {t_begin} is outside [0, {T}]")
+        stride = tok.stride(0) if B > 1 else T
+        if stride < T:
+            raise ValueError(f"the sequences overlap: row stride {stride} below T = {T}")
+        return B, T, stride
+
+    def embed(self, tok, E, *, t_begin: int = 0, scale: float = 1.0, out=None, stream=None):
+        """Hidden states scale * E[tok] of positions t_begin .. T-1: [B*L][d]."""
+        import torch
+        B, T, stride = self._want_tokens(tok, t_begin)
+        n, d = B * (T - t_begin), self.cfg.hidden
+        self._want("E", E, (self.cfg.vocab, d), self.dtype)
+        with _on_stream(stream):
+            h = torch.empty(n, d, dtype=self.dtype, device=self.device) if out is None else out
+        self._want("out", h, (n, d), self.dtype)
+        engram_embed(self.ctx, tok, B, T, stride, t_begin, E, scale, h, stream)
+        return h
+
+    def embed_grad(self, tok, d_h, *, t_begin: int = 0, scale: float = 1.0, out=None, accumulate: bool = False,
+                   stream=None):
+        """Gradient of E from that of the hidden states: fp32 [V][d], written
+        to `out` (or a new tensor), or added to `out` with accumulate."""
+        import torch
+        B, T, stride = self._want_tokens(tok, t_begin)
+        n, d = B * (T - t_begin), self.cfg.hidden
+        self._want("d_h", d_h, (n, d), self.dtype)
+        if accumulate and out is None:
+            raise ValueError("accumulate needs the gradient to add to (out)")
+        if n > 1 << 24:
+            raise ValueError(f"{n} rows, at most 2^24 in one call")
+        with _on_stream(stream):
+            d_E = torch.empty(self.cfg.vocab, d, dtype=torch.float32, device=self.device) if out is None else out
+            need = engram_embed_grad_workspace_bytes(self.ctx, n)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._want("out", d_E, (self.cfg.vocab, d), torch.float32)
+        engram_embed_grad(self.ctx, tok, B, T, stride, t_begin, d_h, scale, d_E, accumulate, ws, need, stream)
+        return d_E
+
+    def add_norm(self, x, res=None, *, gain=None, sum: bool = True, y: bool = True, q: bool = False,
+                 rstd: bool = False, stream=None) -> NormOut:
+        """s = x + res and its RMSNorm: the sum, the normed rows (y), their E4M3
+        form with a scale per row (q), and 1/rms per row (rstd, for the
+        backward), as asked for."""
+        import torch
+        d = self.cfg.hidden
+        n = x.shape[0]
+        self._want("x", x, (n, d), self.dtype)
+        if res is not None:
+            self._want("res", res, (n, d), self.dtype)
+        if gain is not None:
+            self._want("gain", gain, (d,), torch.float32)
+        with _on_stream(stream):
+            def new(on, *shape, dtype=self.dtype):
+                return torch.empty(*shape, dtype=dtype, device=self.device) if on else None
+            o = NormOut(new(sum, n, d), new(y, n, d), new(q, n, d, dtype=torch.float8_e4m3fn),
+                        new(q, n, dtype=torch.float32), new(rstd, n, dtype=torch.float32))
+        engram_add_norm(self.ctx, x, res, n, gain, o.sum, o.y, o.q, o.q_scale, o.rstd, stream)
+        return o
+
+    def add_norm_grad(self, d_y, sum, rstd, *, gain=None, d_sum=None, need_gain: bool = True, stream=None):
+        """(d_x, d_gain): d_x is the gradient of x and of res; d_gain is None
+        without need_gain."""
+        import torch
+        d = self.cfg.hidden
+        n = d_y.shape[0]
+        self._want("d_y", d_y, (n, d), self.dtype)
+        self._want("sum", sum, (n, d), self.dtype)
+        self._want("rstd", rstd, (n,), torch.float32)
+        if d_sum is not None:
+            self._want("d_sum", d_sum, (n, d), self.dtype)
+        if gain is not None:
+            self._want("gain", gain, (d,), torch.float32)
+        with _on_stream(stream):
+            d_x = torch.empty_like(d_y)
+            d_gain = torch.empty(d, dtype=torch.float32, device=self.device) if need_gain else None
+            need = engram_add_norm_grad_workspace_bytes(self.ctx, n) if need_gain else 0
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need_gain else None
+        engram_add_norm_grad(self.ctx, d_y, d_sum, sum, rstd, n, gain, d_x, d_gain, ws, need, stream)
+        return d_x, d_gain
 
     def status(self, stream=None):
         return engram_device_status(self.ctx, stream)

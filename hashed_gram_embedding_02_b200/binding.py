@@ -43,7 +43,9 @@ EXPORTS = ("engram_create", "engram_destroy", "engram_strerror", "engram_last_er
            "engram_shard_range", "engram_forward_sharded", "engram_ipc_export", "engram_ipc_open", "engram_ipc_close",
            "engram_multibranch_workspace_bytes", "engram_forward_multibranch", "engram_table_grad_workspace_bytes",
            "engram_table_grad", "engram_table_sgd", "engram_host_tier_map", "engram_grad_route_workspace_bytes",
-           "engram_grad_route", "engram_grad_combine_workspace_bytes", "engram_grad_combine", "engram_shard_sgd")
+           "engram_grad_route", "engram_grad_combine_workspace_bytes", "engram_grad_combine", "engram_shard_sgd",
+           "engram_embed", "engram_embed_grad_workspace_bytes", "engram_embed_grad", "engram_add_norm",
+           "engram_add_norm_grad_workspace_bytes", "engram_add_norm_grad")
 ENGRAM_MAX_BRANCHES = 4
 ENGRAM_IPC_HANDLE_BYTES = 64
 ENGRAM_MAX_SHARDS = 16
@@ -128,6 +130,12 @@ _sigs = {
     "engram_ipc_export": ([_vp, _vp, ctypes.POINTER(ctypes.c_uint64)], _st),
     "engram_ipc_open": ([_vp, ctypes.c_uint64, ctypes.POINTER(_vp), ctypes.POINTER(_vp)], _st),
     "engram_ipc_close": ([_vp], _st),
+    "engram_embed": ([_vp, _vp, _i32, _i32, _i64, _i32, _vp, ctypes.c_float, _vp, _vp], _st),
+    "engram_embed_grad_workspace_bytes": ([_vp, _i64], _sz),
+    "engram_embed_grad": ([_vp, _vp, _i32, _i32, _i64, _i32, _vp, ctypes.c_float, _vp, _i32, _vp, _sz, _vp], _st),
+    "engram_add_norm": ([_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _st),
+    "engram_add_norm_grad_workspace_bytes": ([_vp, _i64], _sz),
+    "engram_add_norm_grad": ([_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _st),
     "engram_forward_host": ([_vp, _vp, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                              _i32, _vp, _sz, _vp], _st),
 }
@@ -336,6 +344,39 @@ def engram_grad_combine(ctx, n_shards, shard, pair_rows, pair_grad, n_pairs, row
 def engram_shard_sgd(ctx, n_shards, shard, rows, grad, n_unique, max_rows, shard_table, lr, stream=None):
     _check(_lib.engram_shard_sgd(ctx, n_shards, shard, _ptr(rows), _ptr(grad), _ptr(n_unique), max_rows,
                                  _ptr(shard_table), float(lr), _stream(stream)), "engram_shard_sgd")
+
+
+# ---------------------------------------------------------------- residual stream around the module
+
+def engram_embed(ctx, tok, B, T, tok_stride, t_begin, E, scale, h, stream=None):
+    _check(_lib.engram_embed(ctx, _ptr(tok), B, T, tok_stride, t_begin, _ptr(E), float(scale), _ptr(h),
+                             _stream(stream)), "engram_embed")
+
+
+def engram_embed_grad_workspace_bytes(ctx, n_tok: int) -> int:
+    return int(_lib.engram_embed_grad_workspace_bytes(ctx, n_tok))
+
+
+def engram_embed_grad(ctx, tok, B, T, tok_stride, t_begin, d_h, scale, d_E, accumulate, workspace, workspace_bytes,
+                      stream=None):
+    _check(_lib.engram_embed_grad(ctx, _ptr(tok), B, T, tok_stride, t_begin, _ptr(d_h), float(scale), _ptr(d_E),
+                                  int(accumulate), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "engram_embed_grad")
+
+
+def engram_add_norm(ctx, x, res, n, gain, sum_out, y, q, q_scale, rstd, stream=None):
+    _check(_lib.engram_add_norm(ctx, _ptr(x), _ptr(res), n, _ptr(gain), _ptr(sum_out), _ptr(y), _ptr(q),
+                                _ptr(q_scale), _ptr(rstd), _stream(stream)), "engram_add_norm")
+
+
+def engram_add_norm_grad_workspace_bytes(ctx, n: int) -> int:
+    return int(_lib.engram_add_norm_grad_workspace_bytes(ctx, n))
+
+
+def engram_add_norm_grad(ctx, d_y, d_sum, sum, rstd, n, gain, d_x, d_gain, workspace, workspace_bytes, stream=None):
+    _check(_lib.engram_add_norm_grad(ctx, _ptr(d_y), _ptr(d_sum), _ptr(sum), _ptr(rstd), n, _ptr(gain), _ptr(d_x),
+                                     _ptr(d_gain), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "engram_add_norm_grad")
 
 
 # ---------------------------------------------------------------- sharded tables

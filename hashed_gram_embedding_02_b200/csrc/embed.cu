@@ -1,0 +1,704 @@
+// Token embedding of the hidden states and its gradient.
+//
+//   forward    h[i] = scale * E[tok_i]                     (fp32 product, one rounding)
+//   gradient   dE[v] = scale * sum_{i : tok_i = v} dh[i]   (fp32 sums)
+//
+// Both move rows and compute next to nothing: the forward is bound by the
+// bytes of the rows read and written, the gradient by dh and dE.
+//
+// The gradient sorts the tokens first, so that every sum runs over a
+// contiguous list in increasing position and no float atomics are needed:
+//   1. sort (token, position) by token, stable: least significant digit
+//      first, kDigitBits per pass.  A pass cuts the list into at most
+//      kMaxSortCtas contiguous parts; part p's digit counts are in
+//      hist[p][digit]; its CTA sums the counts of the parts before it and
+//      scatters its elements in order.  The counts of the next pass are made
+//      by the scatter of this one.  At most kSortSmall positions are sorted
+//      by one CTA in shared memory instead.
+//   2. reduce: a piece is `piece` consecutive sorted entries, all columns.
+//      A run of equal tokens that lies inside a piece is summed and stored; a
+//      run cut by a piece's edge leaves its part's sum in `part`.  Work is
+//      the same for every piece however often a token occurs, so a token that
+//      takes half of the batch costs nothing extra.
+//   3. join: the parts of each cut run, in order.
+// The order of every sum depends on the tokens alone.
+#include <algorithm>
+
+#include "ctx.cuh"
+
+namespace engram {
+namespace {
+
+// ---------------------------------------------------------------- row geometry
+
+// Threads of a CTA over rows of `cpr` 16-byte chunks: TPR threads per row
+// (whole warps, or a power of two below a warp), RB rows side by side.
+struct RowGeo {
+    int tpr, rb;
+};
+
+RowGeo row_geo(int cpr) {
+    RowGeo g{};
+    if (cpr >= 32) {
+        g.tpr = std::min(512, (cpr + 31) / 32 * 32);
+        // two equal rounds rather than one full and one short
+        if (cpr > 512) {
+            const int rounds = (cpr + 511) / 512;
+            g.tpr = ((cpr + rounds - 1) / rounds + 31) / 32 * 32;
+        }
+    } else {
+        g.tpr = 1;
+        while (g.tpr < cpr) g.tpr <<= 1;
+    }
+    g.rb = std::max(1, 256 / g.tpr);
+    return g;
+}
+
+// position i of the call -> its token (rows are sequence-major)
+struct TokSource {
+    const int32_t* tok;
+    int64_t stride;
+    int32_t t_begin, L, V;
+    __device__ __forceinline__ int32_t at(int64_t i) const {
+        const int64_t b = i / L;
+        return __ldg(tok + b * stride + t_begin + (i - b * L));
+    }
+};
+
+// ---------------------------------------------------------------- forward
+
+// One CTA takes `rb` groups of RPT rows; a thread holds one 16-byte chunk of
+// each of its RPT rows in flight.
+template <typename T, int RPT>
+__global__ void embed_kernel(TokSource src, int64_t n, const T* __restrict__ E, float scale, T* __restrict__ h,
+                             int cpr, uint32_t* status) {
+    constexpr int EPC = Vec<T>::N;
+    const int64_t row0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * RPT;
+    const T* from[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        from[r] = nullptr;
+        if (row0 + r < n) {
+            const int32_t v = src.at(row0 + r);
+            if (v >= 0 && v < src.V) from[r] = E + (int64_t)v * cpr * EPC;
+            else if (threadIdx.x == 0) flag(status, ENGRAM_ERR_TOKEN);
+        }
+    }
+    for (int c = threadIdx.x; c < cpr; c += blockDim.x) {
+        uint4 q[RPT];
+#pragma unroll
+        for (int r = 0; r < RPT; ++r)
+            q[r] = from[r] ? __ldg(reinterpret_cast<const uint4*>(from[r]) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+            if (row0 + r >= n) break;
+            float f[EPC];
+            Vec<T>::load(reinterpret_cast<const T*>(&q[r]), f);
+#pragma unroll
+            for (int k = 0; k < EPC; ++k) f[k] *= scale;
+            Vec<T>::store(h + ((row0 + r) * cpr + c) * EPC, f);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_embed(const TokSource& src, int64_t n, const void* E, float scale, void* h, int d, int num_sms,
+                         uint32_t* status, cudaStream_t s) {
+    const int cpr = d / Vec<T>::N;
+    const RowGeo g = row_geo(cpr);
+    const dim3 block(g.tpr, g.rb);
+    if (n >= (int64_t)num_sms * 16 * g.rb) {
+        constexpr int RPT = 4;
+        const int64_t per = (int64_t)g.rb * RPT;
+        embed_kernel<T, RPT><<<(unsigned)((n + per - 1) / per), block, 0, s>>>(
+            src, n, static_cast<const T*>(E), scale, static_cast<T*>(h), cpr, status);
+    } else {
+        embed_kernel<T, 1><<<(unsigned)((n + g.rb - 1) / g.rb), block, 0, s>>>(
+            src, n, static_cast<const T*>(E), scale, static_cast<T*>(h), cpr, status);
+    }
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- sort
+
+constexpr int kDigitBits = 9;
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kSortThreads = 256;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortIpt = 4;                                // elements per thread and tile
+constexpr int kSortTile = kSortThreads * kSortIpt;
+constexpr int kMaxSortCtas = 256;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallIpt = 4;
+constexpr int kSortSmall = kSmallThreads * kSmallIpt;      // 2048
+constexpr int64_t kMaxEmbedRows = (int64_t)1 << 24;
+
+// tokens outside [0, V) sort behind all others as V
+__device__ __forceinline__ uint32_t sort_key(const TokSource& src, int64_t i, uint32_t* status) {
+    const int32_t v = src.at(i);
+    if (v >= 0 && v < src.V) return (uint32_t)v;
+    flag(status, ENGRAM_ERR_TOKEN);
+    return (uint32_t)src.V;
+}
+
+// Rank of the warp's 32 elements among the earlier ones of the warp with the
+// same digit: cnt[digit] is the count so far; one lane per digit adds to it.
+__device__ __forceinline__ uint32_t warp_rank(uint32_t digit, bool live, uint32_t* cnt, int lane) {
+    const uint32_t mask = __match_any_sync(0xffffffffu, live ? digit : 0xffffffffu);
+    const uint32_t before = __popc(mask & ((1u << lane) - 1u));
+    const uint32_t had = live ? cnt[digit] : 0u;
+    __syncwarp();
+    if (live && before == 0) cnt[digit] = had + __popc(mask);
+    __syncwarp();
+    return had + before;
+}
+
+// Clears the scratch the later launches count in, and copies the keys out.
+__global__ void embed_keys_kernel(TokSource src, int64_t n, int64_t per, uint32_t* __restrict__ keys,
+                                  uint32_t* __restrict__ pos, uint32_t* __restrict__ hist, uint32_t* hist_next,
+                                  int64_t hist_next_words, uint32_t* touched, int64_t touched_words, uint32_t* count,
+                                  uint32_t* status) {
+    __shared__ uint32_t s_hist[kDigits];
+    for (int k = threadIdx.x; k < kDigits; k += blockDim.x) s_hist[k] = 0;
+    const int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, gs = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t k = g0; k < hist_next_words; k += gs) hist_next[k] = 0;
+    for (int64_t k = g0; k < touched_words; k += gs) touched[k] = 0;
+    if (g0 == 0) *count = 0;
+    __syncthreads();
+    const int64_t lo = blockIdx.x * per, hi = min(n, lo + per);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+        const uint32_t k = sort_key(src, i, status);
+        keys[i] = k;
+        pos[i] = (uint32_t)i;
+        atomicAdd(&s_hist[k & (kDigits - 1)], 1u);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < kDigits; k += blockDim.x) hist[(int64_t)blockIdx.x * kDigits + k] = s_hist[k];
+}
+
+// One pass: stable scatter by the digit at `shift`.  hist_next (nullable):
+// counts of the next digit per part of the output.  touched (last pass):
+// bitmap of the tokens that occur.
+__global__ void __launch_bounds__(kSortThreads)
+embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, int64_t per,
+                     int shift, const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
+                     uint32_t* __restrict__ pos_out, uint32_t* hist_next, uint32_t* touched) {
+    __shared__ uint32_t s_base[kDigits];                   // where this part's next element of a digit goes
+    __shared__ uint32_t s_cnt[kSortWarps][kDigits];
+    __shared__ uint32_t s_scan[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int parts = gridDim.x, me = blockIdx.x;
+    // two digits per thread: totals, and the counts of the parts before this one
+    uint32_t tot[2] = {0, 0}, mine[2] = {0, 0};
+    for (int p = 0; p < parts; ++p) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(hist + (int64_t)p * kDigits) + tid);
+        tot[0] += v.x;
+        tot[1] += v.y;
+        if (p < me) {
+            mine[0] += v.x;
+            mine[1] += v.y;
+        }
+    }
+    uint32_t inc = tot[0] + tot[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    uint32_t base = inc - tot[0] - tot[1];
+    for (int w = 0; w < warp; ++w) base += s_scan[w];
+    s_base[2 * tid] = base + mine[0];
+    s_base[2 * tid + 1] = base + tot[0] + mine[1];
+    const int64_t lo = me * per, hi = min(n, lo + per);
+    for (int64_t t0 = lo; t0 < hi; t0 += kSortTile) {
+        __syncthreads();
+        for (int k = tid; k < kSortWarps * kDigits; k += kSortThreads) (&s_cnt[0][0])[k] = 0;
+        __syncthreads();
+        uint32_t key[kSortIpt], ps[kSortIpt], rank[kSortIpt];
+        const int64_t w0 = t0 + warp * (32 * kSortIpt);    // a warp's elements are contiguous
+#pragma unroll
+        for (int k = 0; k < kSortIpt; ++k) {
+            const int64_t i = w0 + k * 32 + lane;
+            key[k] = i < hi ? keys[i] : 0u;
+            ps[k] = i < hi ? pos[i] : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < kSortIpt; ++k)
+            rank[k] = warp_rank((key[k] >> shift) & (kDigits - 1), w0 + k * 32 + lane < hi, s_cnt[warp], lane);
+        __syncthreads();
+        // counts of the warps -> the offset of each warp's first element of a digit
+        for (int g = tid; g < kDigits; g += kSortThreads) {
+            uint32_t run = s_base[g];
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t x = s_cnt[w][g];
+                s_cnt[w][g] = run;
+                run += x;
+            }
+            s_base[g] = run;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSortIpt; ++k) {
+            const int64_t i = w0 + k * 32 + lane;
+            if (i < hi) {
+                const uint32_t to = s_cnt[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k];
+                keys_out[to] = key[k];
+                pos_out[to] = ps[k];
+                if (hist_next)
+                    atomicAdd(hist_next + (to / per) * kDigits + ((key[k] >> (shift + kDigitBits)) & (kDigits - 1)),
+                              1u);
+                if (touched) atomicOr(touched + (key[k] >> 5), 1u << (key[k] & 31));
+            }
+        }
+    }
+}
+
+// At most kSortSmall positions: all passes in one CTA's shared memory.
+__global__ void __launch_bounds__(kSmallThreads)
+embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__ keys_out,
+                        uint32_t* __restrict__ pos_out, uint32_t* touched, int64_t touched_words, uint32_t* count,
+                        uint32_t* status) {
+    __shared__ uint32_t s_key[kSortSmall];
+    __shared__ uint16_t s_pos[kSortSmall];
+    __shared__ uint16_t s_cnt[kSmallWarps][kDigits];
+    __shared__ uint32_t s_scan[kSmallWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int64_t k = tid; k < touched_words; k += kSmallThreads) touched[k] = 0;
+    if (tid == 0) *count = 0;
+    uint32_t key[kSmallIpt], ps[kSmallIpt], rank[kSmallIpt];
+    const int w0 = warp * (32 * kSmallIpt);
+#pragma unroll
+    for (int k = 0; k < kSmallIpt; ++k) {
+        const int i = w0 + k * 32 + lane;
+        key[k] = i < n ? sort_key(src, i, status) : 0u;
+        ps[k] = (uint32_t)i;
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * kDigitBits;
+        __syncthreads();
+        for (int k = tid; k < kSmallWarps * kDigits; k += kSmallThreads) (&s_cnt[0][0])[k] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmallIpt; ++k) {
+            const bool live = w0 + k * 32 + lane < n;
+            const uint32_t digit = (key[k] >> shift) & (kDigits - 1);
+            const uint32_t mask = __match_any_sync(0xffffffffu, live ? digit : 0xffffffffu);
+            const uint32_t before = __popc(mask & ((1u << lane) - 1u));
+            const uint32_t had = live ? s_cnt[warp][digit] : 0u;
+            __syncwarp();
+            if (live && before == 0) s_cnt[warp][digit] = (uint16_t)(had + __popc(mask));
+            __syncwarp();
+            rank[k] = had + before;
+        }
+        __syncthreads();
+        // one digit per thread: its total, the scan over digits, then the warps' offsets
+        uint32_t tot = 0;
+        for (int w = 0; w < kSmallWarps; ++w) tot += s_cnt[w][tid];
+        uint32_t inc = tot;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        uint32_t run = inc - tot;
+        for (int w = 0; w < warp; ++w) run += s_scan[w];
+        for (int w = 0; w < kSmallWarps; ++w) {
+            const uint32_t x = s_cnt[w][tid];
+            s_cnt[w][tid] = (uint16_t)run;
+            run += x;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmallIpt; ++k) {
+            if (w0 + k * 32 + lane < n) {
+                const uint32_t to = s_cnt[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k];
+                s_key[to] = key[k];
+                s_pos[to] = (uint16_t)ps[k];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmallIpt; ++k) {
+            const int i = w0 + k * 32 + lane;
+            if (i < n) {
+                key[k] = s_key[i];
+                ps[k] = s_pos[i];
+            }
+        }
+    }
+    // the bitmap was cleared above by this CTA alone; the barriers of the passes order the two
+#pragma unroll
+    for (int k = 0; k < kSmallIpt; ++k) {
+        const int i = w0 + k * 32 + lane;
+        if (i < n) {
+            keys_out[i] = key[k];
+            pos_out[i] = ps[k];
+            if (touched) atomicOr(touched + (key[k] >> 5), 1u << (key[k] & 31));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reduce
+
+constexpr int kPieceLong = 32;    // sorted entries per piece
+constexpr int kPieceShort = 8;    // few positions: more pieces in flight
+constexpr int kAhead = 8;         // rows of dh in flight per thread
+
+struct EmbedGrad {
+    const uint32_t* keys;
+    const uint32_t* pos;
+    int64_t n;
+    int64_t n_pieces;
+    uint32_t V;
+    int d;
+    float scale;
+    float* d_E;
+    float* part;                  // [n_pieces][2][d]: a piece's first run when it began earlier, its last when it goes on
+    uint32_t* cut;                // pieces whose last run begins there and goes on
+    uint32_t* count;
+    const uint32_t* touched;
+};
+
+template <int EPC>
+__device__ __forceinline__ void put_row(float* to, const float* f, float scale, bool accumulate) {
+#pragma unroll
+    for (int k = 0; k < EPC; k += 4) {
+        float4 o = make_float4(scale * f[k], scale * f[k + 1], scale * f[k + 2], scale * f[k + 3]);
+        if (accumulate) {
+            const float4 was = *reinterpret_cast<const float4*>(to + k);
+            o.x += was.x;
+            o.y += was.y;
+            o.z += was.z;
+            o.w += was.w;
+        }
+        *reinterpret_cast<float4*>(to + k) = o;
+    }
+}
+
+// blocks [0, piece_blocks): pieces, blockDim.y at a time; the rest: zero the
+// rows of dE whose token does not occur
+template <typename T, int PIECE, bool ACC>
+__global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh, unsigned piece_blocks) {
+    constexpr int EPC = Vec<T>::N;
+    extern __shared__ uint32_t s_mem[];
+    const int cpr = p.d / EPC;
+    if (blockIdx.x >= piece_blocks) {
+        const int64_t nb = gridDim.x - piece_blocks;
+        const int vec = p.d / 4;
+        for (int64_t v = (int64_t)(blockIdx.x - piece_blocks) * blockDim.y + threadIdx.y; v < p.V; v += nb * blockDim.y) {
+            if ((__ldg(p.touched + (v >> 5)) >> (v & 31)) & 1u) continue;
+            float4* row = reinterpret_cast<float4*>(p.d_E + v * p.d);
+            for (int c = threadIdx.x; c < vec; c += blockDim.x) row[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
+    const int64_t piece = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    // keys of the piece with one neighbour on each side (kNone outside the list), and its positions
+    constexpr uint32_t kNone = 0xffffffffu;
+    uint32_t* s_key = s_mem + threadIdx.y * (2 * PIECE + 2);
+    uint32_t* s_pos = s_key + PIECE + 2;
+    const int64_t i0 = piece * PIECE;
+    for (int k = threadIdx.x; k < PIECE + 2; k += blockDim.x) {
+        const int64_t i = i0 + k - 1;
+        s_key[k] = i >= 0 && i < p.n ? p.keys[i] : kNone;
+        if (k > 0 && k <= PIECE) s_pos[k - 1] = i < p.n ? p.pos[i] : 0u;
+    }
+    __syncthreads();
+    if (i0 >= p.n) return;
+    const int len = (int)min((int64_t)PIECE, p.n - i0);
+    const bool enters = s_key[0] == s_key[1];                    // the first run began before this piece
+    const bool leaves = s_key[len] == s_key[len + 1];            // the last run goes on behind it
+    if (threadIdx.x == 0 && leaves && s_key[len] < p.V && !(enters && s_key[1] == s_key[len]))
+        p.cut[atomicAdd(p.count, 1u)] = (uint32_t)piece;
+    float* part = p.part + piece * 2 * p.d;
+    for (int c = threadIdx.x; c < cpr; c += blockDim.x) {
+        float acc[EPC];
+#pragma unroll
+        for (int k = 0; k < EPC; ++k) acc[k] = 0.f;
+        const uint4* from = reinterpret_cast<const uint4*>(dh) + c;
+        bool first = true;
+#pragma unroll 1
+        for (int e0 = 0; e0 < len; e0 += kAhead) {
+            uint4 q[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                q[a] = e0 + a < len ? __ldg(from + (int64_t)s_pos[e0 + a] * cpr) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const int e = e0 + a;
+                if (e >= len) break;
+                float f[EPC];
+                Vec<T>::load(reinterpret_cast<const T*>(&q[a]), f);
+#pragma unroll
+                for (int k = 0; k < EPC; ++k) acc[k] += f[k];
+                const uint32_t key = s_key[e + 1];
+                if (e + 1 == len || s_key[e + 2] != key) {
+                    // the end of a run, or of the piece
+                    if (key < p.V) {
+                        if (first && enters) {
+#pragma unroll
+                            for (int k = 0; k < EPC; k += 4)
+                                *reinterpret_cast<float4*>(part + c * EPC + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+                        } else if (e + 1 == len && leaves) {
+#pragma unroll
+                            for (int k = 0; k < EPC; k += 4)
+                                *reinterpret_cast<float4*>(part + p.d + c * EPC + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+                        } else {
+                            put_row<EPC>(p.d_E + (int64_t)key * p.d + c * EPC, acc, p.scale, ACC);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < EPC; ++k) acc[k] = 0.f;
+                    first = false;
+                }
+            }
+        }
+    }
+}
+
+// The cut runs: a CTA takes 128 columns of one run; its eight warps sum
+// contiguous eighths of the run's parts, which are then added in order.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 128;
+
+template <int PIECE, bool ACC>
+__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(EmbedGrad p) {
+    __shared__ float4 s_sum[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slices = (p.d + kJoinCols - 1) / kJoinCols;
+    const int64_t work = (int64_t)*p.count * slices;
+    for (int64_t u = blockIdx.x; u < work; u += gridDim.x) {
+        const int64_t p0 = p.cut[u / slices];
+        const int col = (int)(u % slices) * kJoinCols + lane * 4;
+        const uint32_t key = p.keys[p0 * PIECE + PIECE - 1];
+        // the last piece the run reaches: pieces after p0 that begin with its token
+        int64_t lo = p0 + 1, hi = p.n_pieces;              // first piece in (p0, n_pieces) that does not
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (p.keys[mid * PIECE] == key) lo = mid + 1;
+            else hi = mid;
+        }
+        const int64_t m = lo - p0;                         // parts: p0's last run, then the first runs of m - 1 pieces
+        const int64_t per = (m + kJoinWarps - 1) / kJoinWarps;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < p.d) {
+            const int64_t a = warp * per, b = min(m, a + per);
+#pragma unroll 8
+            for (int64_t k = a; k < b; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(p.part + (p0 + k) * 2 * p.d + (k == 0 ? p.d : 0) + col);
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+        }
+        s_sum[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0 && col < p.d) {
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 x = s_sum[w][lane];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+            const float f[4] = {acc.x, acc.y, acc.z, acc.w};
+            put_row<4>(p.d_E + (int64_t)key * p.d + col, f, p.scale, ACC);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+int sort_passes(int32_t V) {
+    int bits = 0;
+    while (((int64_t)1 << bits) <= V) ++bits;              // keys 0 .. V
+    return (bits + kDigitBits - 1) / kDigitBits;
+}
+
+int64_t sort_part(int64_t n) {
+    const int64_t parts = std::min<int64_t>(kMaxSortCtas, (n + kSortTile - 1) / kSortTile);
+    return (n + parts - 1) / parts;
+}
+
+int piece_of(int64_t n, int num_sms) { return n >= (int64_t)kPieceLong * num_sms * 4 ? kPieceLong : kPieceShort; }
+
+struct EmbedWs {
+    uint32_t* keys[2];
+    uint32_t* pos[2];
+    uint32_t* hist[2];
+    uint32_t* touched;
+    uint32_t* count;
+    uint32_t* cut;
+    float* part;
+    int64_t hist_words, touched_words, n_pieces;
+    int piece;
+    size_t bytes;
+};
+
+EmbedWs embed_carve(const engram_ctx* c, void* base, int64_t n) {
+    EmbedWs w{};
+    char* p = static_cast<char*>(base);
+    auto take = [&](size_t bytes) {
+        char* q = p;
+        p += align256(bytes);
+        return q;
+    };
+    for (int k = 0; k < 2; ++k) {
+        w.keys[k] = reinterpret_cast<uint32_t*>(take((size_t)n * 4));
+        w.pos[k] = reinterpret_cast<uint32_t*>(take((size_t)n * 4));
+    }
+    if (n > kSortSmall) {
+        const int64_t per = sort_part(n);
+        w.hist_words = (n + per - 1) / per * kDigits;
+        for (int k = 0; k < 2; ++k) w.hist[k] = reinterpret_cast<uint32_t*>(take((size_t)w.hist_words * 4));
+    }
+    w.touched_words = ((int64_t)c->cfg.vocab + 1 + 31) / 32;
+    w.touched = reinterpret_cast<uint32_t*>(take((size_t)w.touched_words * 4));
+    w.count = reinterpret_cast<uint32_t*>(take(4));
+    w.piece = piece_of(n, c->num_sms);
+    w.n_pieces = (n + w.piece - 1) / w.piece;
+    w.cut = reinterpret_cast<uint32_t*>(take((size_t)w.n_pieces * 4));
+    w.part = reinterpret_cast<float*>(take((size_t)w.n_pieces * 2 * c->cfg.hidden * 4));
+    w.bytes = (size_t)(p - static_cast<char*>(base));
+    return w;
+}
+
+template <typename T, int PIECE, bool ACC>
+cudaError_t launch_reduce(const engram_ctx* c, const EmbedGrad& p, const void* dh, cudaStream_t s) {
+    const RowGeo g = row_geo(p.d / Vec<T>::N);
+    const dim3 block(g.tpr, g.rb);
+    const unsigned pieces = (unsigned)((p.n_pieces + g.rb - 1) / g.rb);
+    unsigned fill = 0;
+    if (!ACC) fill = (unsigned)std::min<int64_t>(((int64_t)p.V + g.rb - 1) / g.rb, (int64_t)c->num_sms * 16);
+    const size_t smem = (size_t)g.rb * (2 * PIECE + 2) * 4;
+    embed_reduce_kernel<T, PIECE, ACC><<<pieces + fill, block, smem, s>>>(p, static_cast<const T*>(dh), pieces);
+    return cudaGetLastError();
+}
+
+template <int PIECE, bool ACC>
+cudaError_t reduce_and_join(engram_ctx* c, const EmbedGrad& p, const void* dh, cudaStream_t s) {
+    prof_begin(c, s, "embed_reduce");
+    cudaError_t e = c->hs == 2 ? launch_reduce<__nv_bfloat16, PIECE, ACC>(c, p, dh, s)
+                               : launch_reduce<float, PIECE, ACC>(c, p, dh, s);
+    prof_end(c, s);
+    if (e != cudaSuccess || p.n_pieces < 2) return e;
+    prof_begin(c, s, "embed_join");
+    const int slices = (p.d + kJoinCols - 1) / kJoinCols;
+    const unsigned blocks = (unsigned)std::min<int64_t>(p.n_pieces * slices, (int64_t)c->num_sms * 8);
+    embed_join_kernel<PIECE, ACC><<<blocks, kJoinWarps * 32, 0, s>>>(p);
+    prof_end(c, s);
+    return cudaGetLastError();
+}
+
+engram_status check_tokens(const engram_ctx* c, int32_t B, int32_t T, int64_t tok_stride, int32_t t_begin,
+                           float scale) {
+    engram_status st = check_forward_args(c, B, T, tok_stride, t_begin);
+    if (st != ENGRAM_OK) return st;
+    if (!(scale - scale == 0.f)) return inval("scale must be finite");
+    return ENGRAM_OK;
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" {
+
+engram_status engram_embed(engram_ctx* c, const int32_t* tok, int32_t B, int32_t T, int64_t tok_stride,
+                           int32_t t_begin, const void* E, float scale, void* h, cudaStream_t s) {
+    engram_status st = check_tokens(c, B, T, tok_stride, t_begin, scale);
+    if (st != ENGRAM_OK) return st;
+    const int64_t n = (int64_t)B * (T - t_begin);
+    if (n == 0) return ENGRAM_OK;
+    if (n >= (int64_t)1 << 31) return inval("B * (T - t_begin) must be below 2^31");
+    if (!tok || !E || !h) return inval("null tensor pointer");
+    if (!aligned16(E) || !aligned16(h)) return inval("E and h must be 16-byte aligned");
+    st = check_device(c);
+    if (st != ENGRAM_OK) return st;
+    prof_reset(c);
+    const TokSource src{tok, tok_stride, t_begin, T - t_begin, c->cfg.vocab};
+    prof_begin(c, s, "embed");
+    cudaError_t e = c->hs == 2
+                        ? launch_embed<__nv_bfloat16>(src, n, E, scale, h, c->cfg.hidden, c->num_sms, c->d_status, s)
+                        : launch_embed<float>(src, n, E, scale, h, c->cfg.hidden, c->num_sms, c->d_status, s);
+    prof_end(c, s);
+    return e == cudaSuccess ? ENGRAM_OK : cuda_fail("embedding launch", e);
+}
+
+size_t engram_embed_grad_workspace_bytes(const engram_ctx* c, int64_t n_tok) {
+    if (!c || n_tok < 0 || n_tok > kMaxEmbedRows) return 0;
+    return embed_carve(c, nullptr, std::max<int64_t>(1, n_tok)).bytes;
+}
+
+engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, int32_t T, int64_t tok_stride,
+                                int32_t t_begin, const void* d_h, float scale, float* d_E, int32_t accumulate,
+                                void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    engram_status st = check_tokens(c, B, T, tok_stride, t_begin, scale);
+    if (st != ENGRAM_OK) return st;
+    const int64_t n = (int64_t)B * (T - t_begin);
+    if (n > kMaxEmbedRows) return inval("B * (T - t_begin) must be at most 2^24");
+    if (!d_E) return inval("null gradient pointer");
+    if (n > 0 && (!tok || !d_h || !workspace)) return inval("null tensor pointer");
+    if (!aligned16(d_h) || !aligned16(d_E)) return inval("d_h and d_E must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return inval("workspace must be 256-byte aligned");
+    if (n > 0 && workspace_bytes < embed_carve(c, nullptr, n).bytes) {
+        set_error("engram_embed_grad: the workspace is smaller than engram_embed_grad_workspace_bytes");
+        return ENGRAM_E_NOMEM;
+    }
+    st = check_device(c);
+    if (st != ENGRAM_OK) return st;
+    prof_reset(c);
+    const int64_t V = c->cfg.vocab;
+    const int d = c->cfg.hidden;
+    if (n == 0) {
+        if (accumulate) return ENGRAM_OK;
+        cudaError_t e = cudaMemsetAsync(d_E, 0, (size_t)V * d * 4, s);
+        return e == cudaSuccess ? ENGRAM_OK : cuda_fail("clearing the embedding gradient", e);
+    }
+    EmbedWs w = embed_carve(c, workspace, n);
+    const TokSource src{tok, tok_stride, t_begin, T - t_begin, c->cfg.vocab};
+    const int passes = sort_passes(c->cfg.vocab);
+    uint32_t* touched = accumulate ? nullptr : w.touched;
+    const int64_t touched_words = accumulate ? 0 : w.touched_words;
+    int at = 0;
+    cudaError_t e = cudaSuccess;
+    prof_begin(c, s, "embed_sort");
+    if (n <= kSortSmall) {
+        embed_sort_small_kernel<<<1, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
+                                                            touched_words, w.count, c->d_status);
+    } else {
+        const int64_t per = sort_part(n);
+        const unsigned parts = (unsigned)((n + per - 1) / per);
+        embed_keys_kernel<<<parts, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], w.hist[1],
+                                                         w.hist_words, touched, touched_words, w.count, c->d_status);
+        for (int p = 0; p < passes; ++p) {
+            const bool last = p + 1 == passes;
+            // the counts of pass p + 1 go where those of pass p - 1 were: cleared here from the third pass on
+            if (p > 0 && !last) e = cudaMemsetAsync(w.hist[at ^ 1], 0, (size_t)w.hist_words * 4, s);
+            if (e != cudaSuccess) break;
+            embed_scatter_kernel<<<parts, kSortThreads, 0, s>>>(w.keys[at], w.pos[at], n, per, p * kDigitBits, w.hist[at],
+                                                                w.keys[at ^ 1], w.pos[at ^ 1], last ? nullptr : w.hist[at ^ 1],
+                                                                last ? touched : nullptr);
+            at ^= 1;
+        }
+    }
+    prof_end(c, s);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail("embedding gradient sort launches", e);
+    const EmbedGrad p{w.keys[at], w.pos[at], n, w.n_pieces, (uint32_t)V, d, scale, d_E, w.part, w.cut, w.count, w.touched};
+    if (w.piece == kPieceLong)
+        e = accumulate ? reduce_and_join<kPieceLong, true>(c, p, d_h, s) : reduce_and_join<kPieceLong, false>(c, p, d_h, s);
+    else
+        e = accumulate ? reduce_and_join<kPieceShort, true>(c, p, d_h, s) : reduce_and_join<kPieceShort, false>(c, p, d_h, s);
+    return e == cudaSuccess ? ENGRAM_OK : cuda_fail("embedding gradient launches", e);
+}
+
+}  // extern "C"

@@ -446,6 +446,67 @@ ENGRAM_API engram_status engram_shard_sgd(engram_ctx* ctx, int32_t n_shards, int
                                           const float* grad, const uint64_t* n_unique, int64_t max_rows,
                                           void* shard_table, float lr, cudaStream_t stream);
 
+/* ------------------------------------------------------------ the residual stream around the module
+ *
+ * The module reads hidden states h and its output joins the residual stream
+ * ("DeepSeek AI II" digest, section "DeepSeek Engram": H <- H + Y, then the
+ * layer's other blocks).  These calls are the steps next to it: the hidden
+ * states from the token ids, the residual sum with the norm of the following
+ * block, and that block as a gated feed-forward pair of projections, each
+ * with its backward.  d is the context's hidden width, and "model dtype" is
+ * that of h: fp32 for ENGRAM_F32, bf16 for ENGRAM_BF16 and ENGRAM_FP8.
+ *
+ * engram_embed: h[row][:] = scale * E[tok][:] for the rows of tok as in
+ * engram_forward (sequence-major, positions t_begin .. T-1).  E is [V][d]
+ * (V = the config's vocab), h [B*L][d], both model dtype, 16-byte aligned;
+ * the product is fp32, rounded once.  An id outside [0, V) gives a zero row
+ * and sets ENGRAM_ERR_TOKEN.
+ *
+ * engram_embed_grad: its gradient, d_E[v] = scale * (sum of d_h over the rows
+ * whose token is v), d_E [V][d] fp32 (16-byte aligned), d_h [B*L][d] model
+ * dtype.  accumulate = 0 writes every row of d_E (zero where v does not
+ * occur); otherwise the rows of the tokens that occur are added to and no
+ * other row is touched.  The tokens are sorted and the sums run in fp32 in an
+ * order that depends on the tokens alone, so the result is the same on every
+ * run.  Rows with an id outside [0, V) contribute nothing and set
+ * ENGRAM_ERR_TOKEN.  At most 2^24 rows.  Scratch:
+ * engram_embed_grad_workspace_bytes(ctx, B*L) bytes, 256-byte aligned (0 when
+ * the row count is out of range). */
+ENGRAM_API engram_status engram_embed(engram_ctx* ctx, const int32_t* tok, int32_t B, int32_t T, int64_t tok_stride,
+                                      int32_t t_begin, const void* E, float scale, void* h, cudaStream_t stream);
+ENGRAM_API size_t engram_embed_grad_workspace_bytes(const engram_ctx* ctx, int64_t n_tok);
+ENGRAM_API engram_status engram_embed_grad(engram_ctx* ctx, const int32_t* tok, int32_t B, int32_t T,
+                                           int64_t tok_stride, int32_t t_begin, const void* d_h, float scale,
+                                           float* d_E, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
+/* engram_add_norm: s = x + res (res nullable: s = x) for n rows of d;
+ * sum_out (nullable) gets s rounded to the model dtype; with
+ * r = 1/sqrt(mean(s^2) + eps) of the unrounded fp32 s, y (nullable, model
+ * dtype) gets gain * s * r and rstd (nullable, fp32 [n]) gets r.  q and
+ * q_scale (both or neither) get the same normed row in E4M3: q_scale[row] =
+ * max |gain * s * r| / 448 (fp32) and q = round(gain * s * r / q_scale), bytes
+ * [n][d]; a row of zeros has scale 0 and codes 0, a row that holds a NaN or
+ * an infinity has a NaN scale.  gain is fp32 [d] or null (ones).  sum_out
+ * and y may each be x or res (in place).  Tensors 16-byte aligned; d at most
+ * 32768 (16384 in fp32), else ENGRAM_E_UNSUPPORTED.
+ *
+ * engram_add_norm_grad: from d_y and d_sum (nullable), the gradients that
+ * arrive at y and at sum_out, with sum = sum_out and rstd of the forward:
+ * d_x = d_sum + r * (gain * d_y - sh * mean(gain * d_y * sh)), sh = sum * r
+ * (the gradient of x, and of res); d_gain (nullable, fp32 [d], overwritten) =
+ * sum over rows of d_y * sh, in an order fixed by n and the device.  d_x may
+ * be d_y or d_sum.  Scratch (only with d_gain):
+ * engram_add_norm_grad_workspace_bytes(ctx, n) bytes, 256-byte aligned. */
+ENGRAM_API engram_status engram_add_norm(engram_ctx* ctx, const void* x, const void* res, int64_t n,
+                                         const float* gain, void* sum_out, void* y, void* q, float* q_scale,
+                                         float* rstd, cudaStream_t stream);
+ENGRAM_API size_t engram_add_norm_grad_workspace_bytes(const engram_ctx* ctx, int64_t n);
+ENGRAM_API engram_status engram_add_norm_grad(engram_ctx* ctx, const void* d_y, const void* d_sum, const void* sum,
+                                              const float* rstd, int64_t n, const float* gain, void* d_x,
+                                              float* d_gain, void* workspace, size_t workspace_bytes,
+                                              cudaStream_t stream);
+
 /* engram_forward for callers that cannot allocate device memory (an engine
  * callback where allocation is forbidden, a process whose device memory is
  * all owned by another allocator, a loop that cannot afford cudaMalloc's
