@@ -26,7 +26,8 @@ from .binding import (  # noqa: F401  (re-exported C ABI names)
     engram_table_sgd, engram_host_tier_map, engram_grad_route_workspace_bytes, engram_grad_route,
     engram_grad_combine_workspace_bytes, engram_grad_combine, engram_shard_sgd,
     engram_embed, engram_embed_grad_workspace_bytes, engram_embed_grad, engram_add_norm,
-    engram_add_norm_grad_workspace_bytes, engram_add_norm_grad,
+    engram_add_norm_grad_workspace_bytes, engram_add_norm_grad, engram_ffn_workspace_bytes, engram_ffn,
+    engram_ffn_grad_workspace_bytes, engram_ffn_grad, ENGRAM_ACT_SILU, ENGRAM_ACT_GELU,
     engram_last_error, engram_profile_enable, engram_profile_read, engram_project, engram_remap, engram_strerror,
     engram_workspace_bytes, make_config)
 
@@ -43,6 +44,9 @@ def _on_stream(stream):
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
+
+
+_ACTS = {"silu": ENGRAM_ACT_SILU, "gelu": ENGRAM_ACT_GELU}
 
 
 class NormOut(NamedTuple):
@@ -302,6 +306,59 @@ class Engram:
             ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need_gain else None
         engram_add_norm_grad(self.ctx, d_y, d_sum, sum, rstd, n, gain, d_x, d_gain, ws, need, stream)
         return d_x, d_gain
+
+    def _ffn_args(self, x, Wgu, Wd, act: str, x_dtype, w_dtype):
+        """(n, f, activation code) of a feed-forward call's common tensors."""
+        import torch
+        d = self.cfg.hidden
+        if act not in _ACTS:
+            raise ValueError(f"act is {act!r}, needs one of {sorted(_ACTS)}")
+        if Wd.dim() != 2:
+            raise ValueError(f"Wd has {Wd.dim()} dimensions, needs 2")
+        n, f = x.shape[0], Wd.shape[1]
+        self._want("x", x, (n, d), x_dtype)
+        self._want("Wgu", Wgu, (2 * f, d), w_dtype)
+        self._want("Wd", Wd, (d, f), torch.bfloat16)
+        return n, f, _ACTS[act]
+
+    def ffn(self, x, Wgu, Wd, *, act: str = "silu", x_scale=None, gu_scale=None, res=None, save: bool = False,
+            stream=None):
+        """Gated feed-forward block (act(x Wg^T) * x Wu^T) Wd^T (+ res), Wgu the
+        rows of Wg then Wu; in an FP8 context x and Wgu are E4M3 with a scale
+        per row (x_scale, gu_scale).  Returns y, or (y, gu) with save, gu for
+        :meth:`ffn_grad`."""
+        import torch
+        f8 = self.cfg.dtype == ENGRAM_FP8
+        dt = torch.float8_e4m3fn if f8 else torch.bfloat16
+        n, f, a = self._ffn_args(x, Wgu, Wd, act, dt, dt)
+        if (x_scale is None or gu_scale is None) if f8 else (x_scale is not None or gu_scale is not None):
+            raise ValueError("x_scale and gu_scale go with an FP8 context, and are required there")
+        if f8:
+            self._want("x_scale", x_scale, (n,), torch.float32)
+            self._want("gu_scale", gu_scale, (2 * f,), torch.float32)
+        if res is not None:
+            self._want("res", res, (n, self.cfg.hidden), torch.bfloat16)
+        need = engram_ffn_workspace_bytes(self.ctx, n, f)
+        with _on_stream(stream):
+            y = torch.empty(n, self.cfg.hidden, dtype=torch.bfloat16, device=self.device)
+            gu = torch.empty(n, 2 * f, dtype=torch.bfloat16, device=self.device) if save else None
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        engram_ffn(self.ctx, x, x_scale, n, f, a, Wgu, gu_scale, Wd, res, y, gu, ws, need, stream)
+        return (y, gu) if save else y
+
+    def ffn_grad(self, d_y, x, gu, Wgu, Wd, *, act: str = "silu", stream=None):
+        """(d_x, d_Wgu, d_Wd) from the gradient of y and the forward's x and gu."""
+        import torch
+        bf = torch.bfloat16
+        n, f, a = self._ffn_args(x, Wgu, Wd, act, bf, bf)
+        self._want("d_y", d_y, (n, self.cfg.hidden), bf)
+        self._want("gu", gu, (n, 2 * f), bf)
+        need = engram_ffn_grad_workspace_bytes(self.ctx, n, f)
+        with _on_stream(stream):
+            d_x, d_Wgu, d_Wd = torch.empty_like(x), torch.empty_like(Wgu), torch.empty_like(Wd)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        engram_ffn_grad(self.ctx, d_y, x, gu, n, f, a, Wgu, Wd, d_x, d_Wgu, d_Wd, ws, need, stream)
+        return d_x, d_Wgu, d_Wd
 
     def status(self, stream=None):
         return engram_device_status(self.ctx, stream)

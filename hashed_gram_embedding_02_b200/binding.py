@@ -45,7 +45,9 @@ EXPORTS = ("engram_create", "engram_destroy", "engram_strerror", "engram_last_er
            "engram_table_grad", "engram_table_sgd", "engram_host_tier_map", "engram_grad_route_workspace_bytes",
            "engram_grad_route", "engram_grad_combine_workspace_bytes", "engram_grad_combine", "engram_shard_sgd",
            "engram_embed", "engram_embed_grad_workspace_bytes", "engram_embed_grad", "engram_add_norm",
-           "engram_add_norm_grad_workspace_bytes", "engram_add_norm_grad")
+           "engram_add_norm_grad_workspace_bytes", "engram_add_norm_grad", "engram_ffn_workspace_bytes", "engram_ffn",
+           "engram_ffn_grad_workspace_bytes", "engram_ffn_grad")
+ENGRAM_ACT_SILU, ENGRAM_ACT_GELU = 0, 1
 ENGRAM_MAX_BRANCHES = 4
 ENGRAM_IPC_HANDLE_BYTES = 64
 ENGRAM_MAX_SHARDS = 16
@@ -136,6 +138,10 @@ _sigs = {
     "engram_add_norm": ([_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _st),
     "engram_add_norm_grad_workspace_bytes": ([_vp, _i64], _sz),
     "engram_add_norm_grad": ([_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _st),
+    "engram_ffn_workspace_bytes": ([_vp, _i64, _i32], _sz),
+    "engram_ffn": ([_vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _st),
+    "engram_ffn_grad_workspace_bytes": ([_vp, _i64, _i32], _sz),
+    "engram_ffn_grad": ([_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _st),
     "engram_forward_host": ([_vp, _vp, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                              _i32, _vp, _sz, _vp], _st),
 }
@@ -377,6 +383,25 @@ def engram_add_norm_grad(ctx, d_y, d_sum, sum, rstd, n, gain, d_x, d_gain, works
     _check(_lib.engram_add_norm_grad(ctx, _ptr(d_y), _ptr(d_sum), _ptr(sum), _ptr(rstd), n, _ptr(gain), _ptr(d_x),
                                      _ptr(d_gain), _ptr(workspace), workspace_bytes, _stream(stream)),
            "engram_add_norm_grad")
+
+
+def engram_ffn_workspace_bytes(ctx, n: int, f: int) -> int:
+    return int(_lib.engram_ffn_workspace_bytes(ctx, n, f))
+
+
+def engram_ffn(ctx, x, x_scale, n, f, act, Wgu, gu_scale, Wd, res, y, gu, workspace, workspace_bytes, stream=None):
+    _check(_lib.engram_ffn(ctx, _ptr(x), _ptr(x_scale), n, f, act, _ptr(Wgu), _ptr(gu_scale), _ptr(Wd), _ptr(res),
+                           _ptr(y), _ptr(gu), _ptr(workspace), workspace_bytes, _stream(stream)), "engram_ffn")
+
+
+def engram_ffn_grad_workspace_bytes(ctx, n: int, f: int) -> int:
+    return int(_lib.engram_ffn_grad_workspace_bytes(ctx, n, f))
+
+
+def engram_ffn_grad(ctx, d_y, x, gu, n, f, act, Wgu, Wd, d_x, d_Wgu, d_Wd, workspace, workspace_bytes, stream=None):
+    _check(_lib.engram_ffn_grad(ctx, _ptr(d_y), _ptr(x), _ptr(gu), n, f, act, _ptr(Wgu), _ptr(Wd), _ptr(d_x),
+                                _ptr(d_Wgu), _ptr(d_Wd), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "engram_ffn_grad")
 
 
 # ---------------------------------------------------------------- sharded tables

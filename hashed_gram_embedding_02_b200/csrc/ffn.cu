@@ -1,0 +1,815 @@
+// Gated feed-forward block on the 5th-generation tensor cores, forward and
+// backward.
+//
+//   forward   g = x Wg^T, u = x Wu^T, a = act(g) u, y = a Wd^T (+ res)
+//   backward  da = dy Wd, dg = da u act'(g), du = da act(g),
+//             dx = [dg du] [Wg; Wu], dW = [dg du]^T x, dWd = dy^T a
+//   act       SiLU g s(g), or GELU in its tanh form g s(2 z), z = sqrt(2/pi)
+//             (g + 0.044715 g^3), s the logistic function
+//
+// Six products, one kernel template over the operands' layouts and the
+// epilogue:
+//   EPI_GLU    gate and up columns of the same channels side by side in one
+//              accumulator; the activation and the product in the epilogue, so
+//              g and u reach global memory only when the backward needs them
+//   EPI_DGLU   da in the accumulator; the epilogue reads g and u and writes
+//              dg, du and a
+//   EPI_OUT    bf16 output, residual added in fp32 before the one rounding
+//   EPI_PART   fp32 partial sums of a split contraction (few rows: the
+//              weights are read once, by all SMs), joined by a second kernel
+// An operand whose contraction index is the row of its matrix (Wd in da, Wgu
+// in dx, both in the weight gradients) is loaded as it lies and multiplied
+// MN-major: nothing is transposed in memory.
+//
+// Persistent, warp-specialised (384 threads): warp 0 TMA producer, warp 1
+// allocates TMEM and issues tcgen05.mma, warps 4-11 epilogue (two warps per
+// TMEM lane quarter, taking turns on 16-column chunks).  Two accumulators of
+// up to 256 columns: the epilogue of a tile overlaps the MMAs of the next.
+// More than 128 rows run on CTA pairs (M = 256, each CTA stages its rows of A
+// and half of the columns of B).  Every wait is bounded as in the projection
+// kernels: on a timeout the status bit is set, the roles leave their loops,
+// copies and MMAs in flight are drained and TMEM is freed.
+#include <algorithm>
+#include <mutex>
+
+#include "ctx.cuh"
+#include "tc.cuh"
+
+namespace engram {
+namespace {
+
+enum { EPI_GLU = 0, EPI_DGLU = 1, EPI_OUT = 2, EPI_PART = 3 };
+
+constexpr int BM = 128;                 // rows per CTA (UMMA M 128, or 256 over a pair)
+constexpr int ROWB = 128;               // bytes of a swizzled shared-memory row: 64 bf16 or 128 E4M3
+constexpr int BK = 64;                  // contraction indices per stage of MN-major (bf16) operands
+constexpr int A_BYTES = BM * ROWB;      // 16 KB
+constexpr int MAX_BN = 256;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 128 + EPI_WARPS * 32;
+constexpr int TMEM_COLS = 512;
+
+template <bool PAIR>
+struct Geo {
+    static constexpr int B_BYTES = (PAIR ? MAX_BN / 2 : MAX_BN) * ROWB;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = PAIR ? 6 : 4;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;   // tiles | barriers | alignment
+};
+
+struct __align__(8) Barriers {
+    uint64_t full[8];
+    uint64_t empty[8];
+    uint64_t pfull[8];    // PAIR, leader: the peer's stage is full
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    volatile int abort_flag;
+    int issued;
+    int consumed;
+    uint32_t peer_abort;
+};
+
+struct FfnParams {
+    int M, N;                   // output rows and columns (EPI_GLU: channels)
+    int kb;                     // stages along the contraction
+    int bn;                     // accumulator columns per tile (EPI_GLU: gate and up together)
+    int n_tiles, m_units, splits, raster;
+    uint32_t idesc;
+    int b_rows;                 // K-major B: rows per box
+    int act;
+    __nv_bfloat16* out;         // GLU: a [M][N]; DGLU: dgu [M][2N]; OUT: [M][N]
+    __nv_bfloat16* a_out;       // DGLU: a [M][N]
+    __nv_bfloat16* gu;          // GLU: [M][2N] or null; DGLU: input
+    const __nv_bfloat16* res;   // OUT: [M][N] or null
+    const float* row_scale;     // FP8: [M]
+    const float* col_scale;     // FP8: [2N]
+    float* part;                // PART: [splits][M][N] (GLU: [splits][M][2N])
+    uint32_t* status;
+};
+
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Barriers* sb, uint32_t* status) {
+    const uint32_t a = smem_u32(bar);
+    auto try_wait = [&]() { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
+    if (try_wait()) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (try_wait()) return true;
+        if (sb->abort_flag) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            flag(status, ENGRAM_ERR_TIMEOUT);
+            sb->abort_flag = 1;
+            if (sb->peer_abort) st_remote_s32(sb->peer_abort, 1);
+            return false;
+        }
+    }
+}
+
+// MN-major operand, 128-byte swizzle: boxes of 64 elements x 64 contraction
+// rows of 128 bytes (8 KB); the leading offset steps from one 64-element box
+// to the next, the stride offset from one group of 8 contraction rows to the next
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFF) >> 4);
+    d |= (uint64_t)((BK * ROWB) >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+template <bool PAIR, bool F8>
+__device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR && F8)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d), "l"(da), "l"(db),
+                     "r"(idesc), "r"(accumulate));
+    else if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d), "l"(da), "l"(db),
+                     "r"(idesc), "r"(accumulate));
+    else if constexpr (F8)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d), "l"(da), "l"(db),
+                     "r"(idesc), "r"(accumulate));
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d), "l"(da), "l"(db),
+                     "r"(idesc), "r"(accumulate));
+}
+
+// ---------------------------------------------------------------- activation
+
+// act(g) and its factor p = act(g) / g (the logistic function of k(g))
+__device__ __forceinline__ float act_p(float g, int act) {
+    // k = g, or 2 sqrt(2/pi) (g + 0.044715 g^3)
+    const float k = act == ENGRAM_ACT_SILU ? g : g * fmaf(0.0713548163f, g * g, 1.5957691216f);
+    return __fdividef(1.f, 1.f + __expf(-k));
+}
+
+// act'(g) = p + g p (1 - p) k'(g)
+__device__ __forceinline__ float act_d(float g, float p, int act) {
+    const float dk = act == ENGRAM_ACT_SILU ? 1.f : fmaf(0.2140644488f, g * g, 1.5957691216f);
+    return fmaf(g * dk * p, 1.f - p, p);
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) { Vec<__nv_bfloat16>::load(p, f); }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) { Vec<__nv_bfloat16>::store(p, f); }
+
+// Eight columns from c of one row, whatever the accumulator's sums came from.
+__device__ __forceinline__ void put_glu8(const FfnParams& p, int64_t row, int c, float* g, float* u) {
+    if (p.gu) {
+        // the backward reads g and u rounded to bf16
+        store8(p.gu + row * 2 * p.N + c, g);
+        store8(p.gu + row * 2 * p.N + p.N + c, u);
+    }
+    float a[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = g[k] * act_p(g[k], p.act) * u[k];
+    store8(p.out + row * p.N + c, a);
+}
+
+__device__ __forceinline__ void put_dglu8(const FfnParams& p, int64_t row, int c, const float* da) {
+    float g[8], u[8], dg[8], du[8], a[8];
+    load8(p.gu + row * 2 * p.N + c, g);
+    load8(p.gu + row * 2 * p.N + p.N + c, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float pr = act_p(g[k], p.act);
+        const float h = g[k] * pr;
+        a[k] = h * u[k];
+        du[k] = da[k] * h;
+        dg[k] = da[k] * u[k] * act_d(g[k], pr, p.act);
+    }
+    store8(p.out + row * 2 * p.N + c, dg);
+    store8(p.out + row * 2 * p.N + p.N + c, du);
+    store8(p.a_out + row * p.N + c, a);
+}
+
+__device__ __forceinline__ void put_out8(const FfnParams& p, int64_t row, int c, float* v) {
+    if (p.res) {
+        float r[8];
+        load8(p.res + row * p.N + c, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += r[k];
+    }
+    store8(p.out + row * p.N + c, v);
+}
+
+// ---------------------------------------------------------------- kernel
+
+// AMN / BMN: the operand is MN-major (contraction index = row of its matrix).
+// GLU: B's two column halves are the gate and up rows of the same channels.
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
+__global__ void __launch_bounds__(THREADS, 1)
+ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
+    using GE = Geo<PAIR>;
+    constexpr int NCTA = PAIR ? 2 : 1;
+    constexpr int STAGES = GE::STAGES;
+    constexpr int KSTEP = F8 ? 128 : 64;        // contraction indices per stage
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    const uint32_t tiles_u32 = smem_u32(smem);
+    Barriers* sb = reinterpret_cast<Barriers*>(smem + STAGES * GE::STAGE_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+    const bool leader = rank == 0;
+    const int unit0 = (int)blockIdx.x / NCTA, step = (int)gridDim.x / NCTA;
+    const int tiles = p.n_tiles * p.m_units;
+    const int num_units = tiles * p.splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sb->full[s], 1);
+            mbar_init(&sb->empty[s], 1);
+            mbar_init(&sb->pfull[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sb->tfull[a], 1);
+            mbar_init(&sb->tempty[a], NCTA * EPI_WARPS);
+        }
+        mbar_init(&sb->drain, 1);
+        sb->abort_flag = 0;
+        sb->issued = 0;
+        sb->consumed = 0;
+        sb->peer_abort = PAIR ? peer_addr(const_cast<const int*>(&sb->abort_flag), rank ^ 1u) : 0u;
+        mbar_fence_init();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sb->tmem_base)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sb->tmem_base)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    tc_fence_before();
+    if constexpr (PAIR) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = sb->tmem_base;
+
+    // unit -> split, row unit and column tile; groups of `raster` row units
+    // share the columns' slice of B while it is in L2
+    struct Where {
+        int split, row, nt;
+    };
+    auto where = [&](int u) {
+        Where w;
+        w.split = u / tiles;
+        const int t = u - w.split * tiles;
+        const int per = p.raster * p.n_tiles;
+        const int g = t / per, local = t - g * per;
+        const int rows_g = min(p.raster, p.m_units - g * p.raster);
+        w.row = g * p.raster + local % rows_g;
+        w.nt = local / rows_g;
+        return w;
+    };
+    auto k_lo = [&](int split) { return (int)((int64_t)p.kb * split / p.splits); };
+
+    if (warp == 0) {
+        // ---------------- TMA producer
+        if (lane == 0) {
+            int it = 0;
+            for (int u = unit0; u < num_units && !sb->abort_flag; u += step) {
+                const Where w = where(u);
+                const int m0 = (w.row * NCTA + (int)rank) * BM;
+                const int kend = k_lo(w.split + 1);
+                // first column (row of B) this CTA stages, and the second slice of GLU on one CTA
+                int n0, n1 = 0;
+                if (GLU) {
+                    n0 = w.nt * (p.bn / 2) + (PAIR ? (int)rank * p.N : 0);
+                    n1 = w.nt * (p.bn / 2) + p.N;
+                } else {
+                    n0 = w.nt * p.bn + (int)rank * (p.bn / 2);
+                }
+                const int bytes = A_BYTES + (PAIR ? p.bn / 2 : p.bn) * ROWB;
+                bool ok = true;
+                for (int kb = k_lo(w.split); kb < kend; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
+                    if (!wait_bounded<PAIR>(&sb->empty[s], ph ^ 1u, sb, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a_dst = tiles_u32 + s * GE::STAGE_BYTES;
+                    const uint32_t b_dst = a_dst + A_BYTES;
+                    const bool remote = PAIR && !leader;
+                    const uint32_t bar = remote ? peer_addr(&sb->pfull[s], 0u) : smem_u32(&sb->full[s]);
+                    auto load = [&](const CUtensorMap* m, uint32_t dst, int x, int y) {
+                        if (remote) tma_load_2d_peer_bar(m, dst, bar, x, y);
+                        else tma_load_2d(m, dst, &sb->full[s], x, y);
+                    };
+                    if (remote) mbar_arrive_expect_tx_remote(bar, bytes);
+                    else mbar_arrive_expect_tx(&sb->full[s], bytes);
+                    const int k0 = kb * KSTEP;
+                    if constexpr (AMN) {
+                        load(&map_a, a_dst, m0, k0);
+                        load(&map_a, a_dst + BK * ROWB, m0 + 64, k0);
+                    } else {
+                        load(&map_a, a_dst, k0, m0);
+                    }
+                    if constexpr (BMN) {
+                        const int cols = PAIR ? p.bn / 2 : p.bn;
+                        for (int c = 0; c < cols; c += 64) load(&map_b, b_dst + c * ROWB, n0 + c, k0);
+                    } else {
+                        load(&map_b, b_dst, k0, n0);
+                        if (GLU && !PAIR) load(&map_b, b_dst + p.b_rows * ROWB, k0, n1);
+                    }
+                    sb->issued = it + 1;
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == 1 && (!PAIR || leader)) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            int it = 0, tc = 0;
+            for (int u = unit0; u < num_units && !sb->abort_flag; u += step, ++tc) {
+                const Where w = where(u);
+                const int acc = tc & 1;
+                const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
+                if (!wait_bounded<PAIR>(&sb->tempty[acc], aph ^ 1u, sb, p.status)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * MAX_BN);
+                const int klo = k_lo(w.split), kend = k_lo(w.split + 1);
+                bool ok = true;
+                for (int kb = klo; kb < kend; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
+                    if (!wait_bounded<PAIR>(&sb->full[s], ph, sb, p.status) ||
+                        (PAIR && !wait_bounded<PAIR>(&sb->pfull[s], ph, sb, p.status))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = tiles_u32 + s * GE::STAGE_BYTES;
+                    const uint64_t da = AMN ? smem_desc_mn(a_addr) : smem_desc_sw128(a_addr);
+                    const uint64_t db = BMN ? smem_desc_mn(a_addr + A_BYTES) : smem_desc_sw128(a_addr + A_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        // 16 contraction indices: 32 bytes inside the swizzled row, or 16 rows of 128 bytes
+                        umma<PAIR, F8>(d_tmem, da + (uint64_t)(kk * (AMN ? 128 : 2)), db + (uint64_t)(kk * (BMN ? 128 : 2)),
+                                       p.idesc, (uint32_t)((kb != klo) | (kk != 0)));
+                    }
+                    if constexpr (PAIR) umma_commit_pair_both(&sb->empty[s]);
+                    else umma_commit(&sb->empty[s]);
+                    sb->consumed = it + 1;
+                }
+                if (!ok) break;
+                if constexpr (PAIR) umma_commit_pair_both(&sb->tfull[acc]);
+                else umma_commit(&sb->tfull[acc]);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t leader_tempty[2] = {PAIR ? peer_addr(&sb->tempty[0], 0u) : 0u, PAIR ? peer_addr(&sb->tempty[1], 0u) : 0u};
+        int tc = 0;
+        for (int u = unit0; u < num_units; u += step, ++tc) {
+            const Where w = where(u);
+            const int acc = tc & 1;
+            const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
+            const bool ok = wait_bounded<PAIR>(&sb->tfull[acc], aph, sb, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
+            const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
+            const bool live = row < p.M;
+            const int width = GLU ? p.bn / 2 : p.bn;       // output columns of the tile
+            const int c_tile = w.nt * width;
+            float rs = 1.f;
+            if (F8 && live) rs = __ldg(p.row_scale + row);
+#pragma unroll 1
+            for (int c = half * 16; c < width; c += 32) {
+                uint32_t x[16], y[16];
+                tmem_ld16(taddr + c, x);
+                if (GLU) tmem_ld16(taddr + width + c, y);
+                tmem_wait_ld(x);
+                if (GLU) tmem_wait_ld(y);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = c_tile + c + h * 8;
+                    if (!live || c + h * 8 >= width || col >= p.N) continue;
+                    float f[8], g[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        f[k] = __uint_as_float(x[h * 8 + k]);
+                        if (GLU) g[k] = __uint_as_float(y[h * 8 + k]);
+                    }
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            f[k] *= rs * __ldg(p.col_scale + col + k);
+                            g[k] *= rs * __ldg(p.col_scale + p.N + col + k);
+                        }
+                    }
+                    if constexpr (EPI == EPI_GLU) put_glu8(p, row, col, f, g);
+                    if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, col, f);
+                    if constexpr (EPI == EPI_OUT) put_out8(p, row, col, f);
+                    if constexpr (EPI == EPI_PART) {
+                        const int64_t ld = GLU ? 2 * (int64_t)p.N : p.N;
+                        float* to = p.part + ((int64_t)w.split * p.M + row) * ld + col;
+                        Vec<float>::store(to, f);
+                        Vec<float>::store(to + 4, f + 4);
+                        if (GLU) {
+                            Vec<float>::store(to + p.N, g);
+                            Vec<float>::store(to + p.N + 4, g + 4);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR && !leader) mbar_arrive_remote(leader_tempty[acc]);
+                else mbar_arrive(&sb->tempty[acc]);
+            }
+        }
+    }
+
+    __syncthreads();
+    bool aborted = sb->abort_flag != 0;
+    if constexpr (PAIR) {
+        cluster_sync_all();
+        aborted = aborted || ld_remote_s32(sb->peer_abort) != 0;
+    }
+    if (aborted) {
+        if (warp == 0 && lane == 0 && (!PAIR || leader)) {
+            for (int it = sb->consumed; it < sb->issued; ++it) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&sb->full[it % STAGES]), (uint32_t)(it / STAGES) & 1u) &&
+                       clock64() - t0 < kWaitCycles) {
+                }
+            }
+            if (PAIR) {
+                const int peer_issued = ld_remote_s32(peer_addr(&sb->issued, 1u));
+                for (int it = sb->consumed; it < peer_issued; ++it) {
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(smem_u32(&sb->pfull[it % STAGES]), (uint32_t)(it / STAGES) & 1u) &&
+                           clock64() - t0 < kWaitCycles) {
+                    }
+                }
+            }
+        }
+        if (warp == 1 && lane == 0 && (!PAIR || leader)) {
+            if constexpr (PAIR) umma_commit_pair_local(&sb->drain);
+            else umma_commit(&sb->drain);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&sb->drain), 0) && clock64() - t0 < kWaitCycles) {
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (PAIR) cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// The partial sums of a split contraction in split order, then the epilogue.
+template <int EPI>
+__global__ void ffn_join_kernel(const FfnParams p) {
+    const int vec = p.N / 8;
+    const int64_t total = (int64_t)p.M * vec;
+    const int64_t ld = EPI == EPI_GLU ? 2 * (int64_t)p.N : p.N;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / vec;
+        const int c = (int)(i - row * vec) * 8;
+        float f[8] = {}, g[8] = {};
+        auto add = [&](float* acc, const float* from) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(from)), b = __ldg(reinterpret_cast<const float4*>(from) + 1);
+            acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+            acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+        };
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            const float* from = p.part + ((int64_t)s * p.M + row) * ld + c;
+            add(f, from);
+            if (EPI == EPI_GLU) add(g, from + p.N);
+        }
+        if constexpr (EPI == EPI_GLU) put_glu8(p, row, c, f, g);
+        if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, c, f);
+        if constexpr (EPI == EPI_OUT) put_out8(p, row, c, f);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+// [rows][cols] row-major operand; boxes of 128 bytes of a row x box_rows rows
+bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows, bool f8) {
+    return make_map(m, base, (uint64_t)rows, (uint64_t)cols, (uint32_t)box_rows, f8);
+}
+
+// How a product is cut: one CTA or a pair per tile, accumulator columns,
+// splits of the contraction.
+struct Plan {
+    bool pair;
+    int bn, m_units, n_tiles, kb, splits;
+    size_t part_bytes;
+};
+
+// M x N outputs (N: channels of GLU) over a contraction of kb stages.
+Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool bmn) {
+    Plan best{};
+    double best_cost = 1e30;
+    const bool pair = M > BM;
+    const int workers = pair ? c->num_sms / 2 : c->num_sms;
+    const int64_t cols = glu ? 2 * N : N;
+    const int step = bmn ? (pair ? 128 : 64) : 32;
+    for (int bn = MAX_BN; bn >= (bmn ? step : 64); bn -= step) {
+        const int width = glu ? bn / 2 : bn;
+        const int64_t m_units = pair ? (M + 2 * BM - 1) / (2 * BM) : 1;
+        const int64_t n_tiles = (N + width - 1) / width;
+        const int64_t tiles = m_units * n_tiles;
+        for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
+            if (splits > 1 && tiles * (splits - 1) >= workers) break;
+            const int64_t waves = (tiles * splits + workers - 1) / workers;
+            // stages in a row, each the larger of its MMAs (256 columns: 1) and its operand bytes
+            const double stage = std::max(bn / 256.0, (A_BYTES + (pair ? bn / 2 : bn) * ROWB) / 49152.0);
+            double cost = waves * ((kb + splits - 1) / splits) * stage;
+            if (splits > 1) cost += 6.0 + (double)splits * M * cols * 8 / (16e3 * 1e3);
+            if (cost < best_cost * 0.999) {
+                best_cost = cost;
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits,
+                            splits > 1 ? align256((size_t)splits * M * cols * 4) : 0};
+            }
+        }
+    }
+    return best;
+}
+
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
+cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, cudaStream_t s) {
+    using GE = Geo<PAIR>;
+    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8>;
+    static std::mutex mu;
+    static int max_units[64] = {};              // CTAs or pairs resident at once, per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = GE::SMEM_BYTES;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 0;
+    if (PAIR) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    int cap = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (max_units[dev] == 0) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM_BYTES);
+            if (e != cudaSuccess) return e;
+            int mc = num_sms;
+            if (PAIR) {
+                cfg.gridDim = dim3((unsigned)(num_sms & ~1), 1, 1);
+                if (cudaOccupancyMaxActiveClusters(&mc, kernel, &cfg) != cudaSuccess || mc < 1) {
+                    cudaGetLastError();
+                    mc = num_sms / 2;
+                }
+            }
+            max_units[dev] = mc;
+        }
+        cap = max_units[dev];
+    }
+    const int64_t units = (int64_t)p.m_units * p.n_tiles * p.splits;
+    if (units >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) * std::min<int64_t>(units, cap)), 1, 1);
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+}
+
+// One product: A [M][K] (or [K][M] with AMN), B [N][K] (or [K][N] with BMN;
+// GLU: [2N][K]), and its epilogue, through partial sums when the plan splits.
+template <int EPI, bool AMN, bool BMN, bool F8 = false>
+cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int64_t N, int64_t K, FfnParams p, float* part,
+                    const char* name, cudaStream_t s) {
+    constexpr bool GLU = EPI == EPI_GLU;
+    const int kstep = F8 ? 128 : 64;
+    const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, BMN);
+    p.M = (int)M;
+    p.N = (int)N;
+    p.kb = pl.kb;
+    p.bn = pl.bn;
+    p.n_tiles = pl.n_tiles;
+    p.m_units = pl.m_units;
+    p.splits = pl.splits;
+    p.raster = 8;
+    p.status = c->d_status;
+    p.part = part;
+    p.b_rows = GLU || pl.pair ? pl.bn / 2 : pl.bn;
+    // fp32 accumulator; formats bf16 (or E4M3: 0); MN-major bits; N / 8; M / 16
+    p.idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
+              ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((pl.pair ? 256 : 128) >> 4) << 24);
+    CUtensorMap ma, mb;
+    const int64_t b_cols = GLU ? 2 * N : N;
+    const bool ok = (AMN ? operand_map(&ma, A, K, M, BK, F8) : operand_map(&ma, A, M, K, BM, F8)) &&
+                    (BMN ? operand_map(&mb, B, K, b_cols, BK, F8) : operand_map(&mb, B, b_cols, K, p.b_rows, F8));
+    if (!ok) return cudaErrorInvalidValue;
+    prof_begin(c, s, name);
+    cudaError_t e;
+    if (pl.splits == 1)
+        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, s)
+                    : launch_one<EPI, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, s);
+    else
+        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, s)
+                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, s);
+    prof_end(c, s);
+    if (e == cudaSuccess && pl.splits > 1) {
+        prof_begin(c, s, "ffn_join");
+        const int64_t threads = M * (N / 8);
+        const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
+        ffn_join_kernel<EPI><<<blocks, 256, 0, s>>>(p);
+        prof_end(c, s);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+// Scratch: the products' shared partial sums, then the intermediate matrices.
+struct FfnWs {
+    float* part;
+    __nv_bfloat16* a;       // [n][f]
+    __nv_bfloat16* dgu;     // [n][2f], backward
+    size_t bytes;
+};
+
+FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad) {
+    const int64_t d = c->cfg.hidden;
+    auto kb = [](int64_t K) { return (int)((K + 63) / 64); };
+    size_t part = 0;
+    if (grad) {
+        part = std::max(part, make_plan(c, n, f, kb(d), false, true).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, true).part_bytes);
+        part = std::max(part, make_plan(c, d, f, kb(n), false, true).part_bytes);
+        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, true).part_bytes);
+    } else {
+        const bool f8 = c->cfg.dtype == ENGRAM_FP8;
+        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(f), false, false).part_bytes);
+    }
+    FfnWs w{};
+    char* p = static_cast<char*>(base);
+    auto take = [&](size_t bytes) {
+        char* q = p;
+        p += align256(bytes);
+        return q;
+    };
+    w.part = reinterpret_cast<float*>(take(part));
+    w.a = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * f * 2));
+    if (grad) w.dgu = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * 2 * f * 2));
+    w.bytes = (size_t)(p - static_cast<char*>(base));
+    return w;
+}
+
+constexpr int32_t kMaxFfnWidth = 1 << 20;
+
+engram_status ffn_shape(const engram_ctx* c, int64_t n, int32_t f, int32_t act, bool grad) {
+    if (!c) return inval("null context");
+    if (n < 0 || n >= (int64_t)1 << 31) return inval("the row count must be in [0, 2^31)");
+    if (f < 8 || f % 8 != 0 || f > kMaxFfnWidth) return inval("f must be a multiple of 8 in [8, 2^20]");
+    if (act != ENGRAM_ACT_SILU && act != ENGRAM_ACT_GELU) return inval("unknown activation");
+    if (c->cfg.dtype == ENGRAM_F32 || (grad && c->cfg.dtype != ENGRAM_BF16)) {
+        set_error(grad ? "the feed-forward backward takes bf16 contexts" : "the feed-forward block runs on the tensor cores (bf16 or FP8)");
+        return ENGRAM_E_UNSUPPORTED;
+    }
+    if (!c->sm100) {
+        set_error("the feed-forward block needs an sm_100 device");
+        return ENGRAM_E_UNSUPPORTED;
+    }
+    return ENGRAM_OK;
+}
+
+engram_status check_ws(const void* workspace, size_t have, size_t need) {
+    if (!workspace) return inval("null workspace");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return inval("workspace must be 256-byte aligned");
+    if (have < need) {
+        set_error("the workspace is smaller than the call needs");
+        return ENGRAM_E_NOMEM;
+    }
+    return ENGRAM_OK;
+}
+
+}  // namespace
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" {
+
+size_t engram_ffn_workspace_bytes(const engram_ctx* c, int64_t n, int32_t f) {
+    if (ffn_shape(c, n, f, ENGRAM_ACT_SILU, false) != ENGRAM_OK) return 0;
+    return ffn_carve(c, nullptr, std::max<int64_t>(1, n), f, false).bytes;
+}
+
+engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int64_t n, int32_t f, int32_t act,
+                         const void* Wgu, const float* gu_scale, const void* Wd, const void* res, void* y, void* gu,
+                         void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    engram_status st = ffn_shape(c, n, f, act, false);
+    if (st != ENGRAM_OK) return st;
+    const bool f8 = c->cfg.dtype == ENGRAM_FP8;
+    if (f8 && gu) return inval("gu is for the backward, which takes bf16 contexts");
+    if (n == 0) return ENGRAM_OK;
+    if (!x || !Wgu || !Wd || !y) return inval("null tensor pointer");
+    if (f8 ? (!x_scale || !gu_scale) : (x_scale || gu_scale))
+        return inval("x_scale and gu_scale go with ENGRAM_FP8, and are required there");
+    if (!aligned16(x) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(res) || !aligned16(y) || !aligned16(gu))
+        return inval("x, Wgu, Wd, res, y and gu must be 16-byte aligned");
+    const FfnWs w = ffn_carve(c, workspace, n, f, false);
+    st = check_ws(workspace, workspace_bytes, w.bytes);
+    if (st == ENGRAM_OK) st = check_device(c);
+    if (st != ENGRAM_OK) return st;
+    prof_reset(c);
+    const int64_t d = c->cfg.hidden;
+    FfnParams p{};
+    p.act = act;
+    p.out = w.a;
+    p.gu = static_cast<__nv_bfloat16*>(gu);
+    p.row_scale = x_scale;
+    p.col_scale = gu_scale;
+    cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up_fp8", s)
+                       : product<EPI_GLU, false, false>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up", s);
+    if (e != cudaSuccess) return cuda_fail("feed-forward gate/up launch", e);
+    FfnParams o{};
+    o.out = static_cast<__nv_bfloat16*>(y);
+    o.res = static_cast<const __nv_bfloat16*>(res);
+    e = product<EPI_OUT, false, false>(c, w.a, Wd, n, d, f, o, w.part, "ffn_down", s);
+    return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward down launch", e);
+}
+
+size_t engram_ffn_grad_workspace_bytes(const engram_ctx* c, int64_t n, int32_t f) {
+    if (ffn_shape(c, n, f, ENGRAM_ACT_SILU, true) != ENGRAM_OK) return 0;
+    return ffn_carve(c, nullptr, std::max<int64_t>(1, n), f, true).bytes;
+}
+
+engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, const void* gu, int64_t n, int32_t f,
+                              int32_t act, const void* Wgu, const void* Wd, void* d_x, void* d_Wgu, void* d_Wd,
+                              void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    engram_status st = ffn_shape(c, n, f, act, true);
+    if (st != ENGRAM_OK) return st;
+    if (!d_Wgu || !d_Wd) return inval("null weight gradient");
+    if (n > 0 && (!d_y || !x || !gu || !Wgu || !Wd || !d_x)) return inval("null tensor pointer");
+    if (!aligned16(d_y) || !aligned16(x) || !aligned16(gu) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(d_x) ||
+        !aligned16(d_Wgu) || !aligned16(d_Wd))
+        return inval("tensors must be 16-byte aligned");
+    FfnWs w{};
+    if (n > 0) {
+        w = ffn_carve(c, workspace, n, f, true);
+        st = check_ws(workspace, workspace_bytes, w.bytes);
+        if (st != ENGRAM_OK) return st;
+    }
+    st = check_device(c);
+    if (st != ENGRAM_OK) return st;
+    prof_reset(c);
+    const int64_t d = c->cfg.hidden;
+    if (n == 0) {
+        cudaError_t e = cudaMemsetAsync(d_Wgu, 0, (size_t)2 * f * d * 2, s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(d_Wd, 0, (size_t)f * d * 2, s);
+        return e == cudaSuccess ? ENGRAM_OK : cuda_fail("clearing the weight gradients", e);
+    }
+    FfnParams p{};
+    p.act = act;
+    p.out = w.dgu;
+    p.a_out = w.a;
+    p.gu = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(gu));
+    cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, Wd, n, f, d, p, w.part, "ffn_d_gate_up", s);
+    FfnParams o{};
+    if (e == cudaSuccess) {
+        o.out = static_cast<__nv_bfloat16*>(d_x);
+        e = product<EPI_OUT, false, true>(c, w.dgu, Wgu, n, d, 2 * (int64_t)f, o, w.part, "ffn_d_x", s);
+    }
+    if (e == cudaSuccess) {
+        o.out = static_cast<__nv_bfloat16*>(d_Wgu);
+        e = product<EPI_OUT, true, true>(c, w.dgu, x, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", s);
+    }
+    if (e == cudaSuccess) {
+        o.out = static_cast<__nv_bfloat16*>(d_Wd);
+        e = product<EPI_OUT, true, true>(c, d_y, w.a, d, f, n, o, w.part, "ffn_d_Wd", s);
+    }
+    return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward backward launches", e);
+}
+
+}  // extern "C"

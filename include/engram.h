@@ -507,6 +507,50 @@ ENGRAM_API engram_status engram_add_norm_grad(engram_ctx* ctx, const void* d_y, 
                                               float* d_gain, void* workspace, size_t workspace_bytes,
                                               cudaStream_t stream);
 
+/* Gated feed-forward block of n rows: with g = x Wg^T and u = x Wu^T,
+ *   y = (act(g) * u) Wd^T (+ res),
+ * act one of engram_act: SiLU g / (1 + exp(-g)), or GELU in its tanh form
+ * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).  Runs on the tensor cores,
+ * fp32 accumulation: contexts of ENGRAM_BF16 or ENGRAM_FP8 (ENGRAM_F32:
+ * ENGRAM_E_UNSUPPORTED).
+ *   x    [n][d] bf16, or E4M3 with x_scale [n] fp32 per row (engram_add_norm's
+ *        q and q_scale) in an FP8 context;
+ *   Wgu  [2f][d]: the rows of Wg, then those of Wu; bf16, or E4M3 with
+ *        gu_scale [2f] fp32 per row in an FP8 context (x_scale and gu_scale
+ *        null otherwise);
+ *   Wd   [d][f] bf16 in both; the product act(g) * u is held in bf16 (an
+ *        8-bit product would need its rows' largest value before the first
+ *        one is stored);
+ *   res  [n][d] bf16 or null, added in fp32 before y's one rounding;
+ *   y    [n][d] bf16; may be res or x;
+ *   gu   [n][2f] bf16 or null: g and u, for the backward (bf16 contexts).
+ * f is a multiple of 8, all tensors 16-byte aligned.  Scratch:
+ * engram_ffn_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
+ *
+ * engram_ffn_grad, from the gradient d_y of y (that of res is d_y itself) and
+ * the forward's x and gu:
+ *   da = d_y Wd, dg = da * u * act'(g), du = da * act(g);
+ *   d_x [n][d] = [dg du] Wgu, d_Wgu [2f][d] = [dg du]^T x,
+ *   d_Wd [d][f] = d_y^T (act(g) * u),
+ * all bf16, each sum in fp32 and rounded once when stored (dg, du and
+ * act(g) * u are held in bf16 between the products); d_Wgu and d_Wd are
+ * overwritten.  d_x must not overlap the inputs.  ENGRAM_BF16 contexts only.
+ * Scratch: engram_ffn_grad_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
+ *
+ * The workspace sizes are 0 for arguments the call refuses.  Results are the
+ * same on every run. */
+typedef enum engram_act { ENGRAM_ACT_SILU = 0, ENGRAM_ACT_GELU = 1 } engram_act;
+ENGRAM_API size_t engram_ffn_workspace_bytes(const engram_ctx* ctx, int64_t n, int32_t f);
+ENGRAM_API engram_status engram_ffn(engram_ctx* ctx, const void* x, const float* x_scale, int64_t n, int32_t f,
+                                    int32_t act, const void* Wgu, const float* gu_scale, const void* Wd,
+                                    const void* res, void* y, void* gu, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+ENGRAM_API size_t engram_ffn_grad_workspace_bytes(const engram_ctx* ctx, int64_t n, int32_t f);
+ENGRAM_API engram_status engram_ffn_grad(engram_ctx* ctx, const void* d_y, const void* x, const void* gu, int64_t n,
+                                         int32_t f, int32_t act, const void* Wgu, const void* Wd, void* d_x,
+                                         void* d_Wgu, void* d_Wd, void* workspace, size_t workspace_bytes,
+                                         cudaStream_t stream);
+
 /* engram_forward for callers that cannot allocate device memory (an engine
  * callback where allocation is forbidden, a process whose device memory is
  * all owned by another allocator, a loop that cannot afford cudaMalloc's
