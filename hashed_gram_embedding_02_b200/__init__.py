@@ -27,7 +27,7 @@ from .binding import (  # noqa: F401  (re-exported C ABI names)
     engram_grad_combine_workspace_bytes, engram_grad_combine, engram_shard_sgd,
     engram_embed, engram_embed_grad_workspace_bytes, engram_embed_grad, engram_add_norm,
     engram_add_norm_grad_workspace_bytes, engram_add_norm_grad, engram_ffn_workspace_bytes, engram_ffn,
-    engram_ffn_grad_workspace_bytes, engram_ffn_grad, ENGRAM_ACT_SILU, ENGRAM_ACT_GELU,
+    engram_ffn_saved_bytes, engram_ffn_grad_workspace_bytes, engram_ffn_grad, ENGRAM_ACT_SILU, ENGRAM_ACT_GELU,
     engram_last_error, engram_profile_enable, engram_profile_read, engram_project, engram_remap, engram_strerror,
     engram_workspace_bytes, make_config)
 
@@ -325,8 +325,8 @@ class Engram:
             stream=None):
         """Gated feed-forward block (act(x Wg^T) * x Wu^T) Wd^T (+ res), Wgu the
         rows of Wg then Wu; in an FP8 context x and Wgu are E4M3 with a scale
-        per row (x_scale, gu_scale).  Returns y, or (y, gu) with save, gu for
-        :meth:`ffn_grad`."""
+        per row (x_scale, gu_scale).  Returns y, or (y, saved) with save: the
+        bytes that :meth:`ffn_grad` reads (bf16 contexts)."""
         import torch
         f8 = self.cfg.dtype == ENGRAM_FP8
         dt = torch.float8_e4m3fn if f8 else torch.bfloat16
@@ -341,23 +341,23 @@ class Engram:
         need = engram_ffn_workspace_bytes(self.ctx, n, f)
         with _on_stream(stream):
             y = torch.empty(n, self.cfg.hidden, dtype=torch.bfloat16, device=self.device)
-            gu = torch.empty(n, 2 * f, dtype=torch.bfloat16, device=self.device) if save else None
+            saved = torch.empty(engram_ffn_saved_bytes(self.ctx, n, f), dtype=torch.uint8, device=self.device) if save else None
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        engram_ffn(self.ctx, x, x_scale, n, f, a, Wgu, gu_scale, Wd, res, y, gu, ws, need, stream)
-        return (y, gu) if save else y
+        engram_ffn(self.ctx, x, x_scale, n, f, a, Wgu, gu_scale, Wd, res, y, saved, ws, need, stream)
+        return (y, saved) if save else y
 
-    def ffn_grad(self, d_y, x, gu, Wgu, Wd, *, act: str = "silu", stream=None):
-        """(d_x, d_Wgu, d_Wd) from the gradient of y and the forward's x and gu."""
+    def ffn_grad(self, d_y, x, saved, Wgu, Wd, *, act: str = "silu", stream=None):
+        """(d_x, d_Wgu, d_Wd) from the gradient of y and the forward's x and saved."""
         import torch
         bf = torch.bfloat16
         n, f, a = self._ffn_args(x, Wgu, Wd, act, bf, bf)
         self._want("d_y", d_y, (n, self.cfg.hidden), bf)
-        self._want("gu", gu, (n, 2 * f), bf)
+        self._want("saved", saved, (n * f * 2 + (n + 31) // 32 * 32 * f * 6,), torch.uint8)
         need = engram_ffn_grad_workspace_bytes(self.ctx, n, f)
         with _on_stream(stream):
             d_x, d_Wgu, d_Wd = torch.empty_like(x), torch.empty_like(Wgu), torch.empty_like(Wd)
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        engram_ffn_grad(self.ctx, d_y, x, gu, n, f, a, Wgu, Wd, d_x, d_Wgu, d_Wd, ws, need, stream)
+        engram_ffn_grad(self.ctx, d_y, x, saved, n, f, a, Wgu, Wd, d_x, d_Wgu, d_Wd, ws, need, stream)
         return d_x, d_Wgu, d_Wd
 
     def status(self, stream=None):

@@ -46,7 +46,7 @@ EXPORTS = ("engram_create", "engram_destroy", "engram_strerror", "engram_last_er
            "engram_grad_route", "engram_grad_combine_workspace_bytes", "engram_grad_combine", "engram_shard_sgd",
            "engram_embed", "engram_embed_grad_workspace_bytes", "engram_embed_grad", "engram_add_norm",
            "engram_add_norm_grad_workspace_bytes", "engram_add_norm_grad", "engram_ffn_workspace_bytes", "engram_ffn",
-           "engram_ffn_grad_workspace_bytes", "engram_ffn_grad")
+           "engram_ffn_saved_bytes", "engram_ffn_grad_workspace_bytes", "engram_ffn_grad")
 ENGRAM_ACT_SILU, ENGRAM_ACT_GELU = 0, 1
 ENGRAM_MAX_BRANCHES = 4
 ENGRAM_IPC_HANDLE_BYTES = 64
@@ -140,6 +140,7 @@ _sigs = {
     "engram_add_norm_grad": ([_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp], _st),
     "engram_ffn_workspace_bytes": ([_vp, _i64, _i32], _sz),
     "engram_ffn": ([_vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _st),
+    "engram_ffn_saved_bytes": ([_vp, _i64, _i32], _sz),
     "engram_ffn_grad_workspace_bytes": ([_vp, _i64, _i32], _sz),
     "engram_ffn_grad": ([_vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _st),
     "engram_forward_host": ([_vp, _vp, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
@@ -389,17 +390,21 @@ def engram_ffn_workspace_bytes(ctx, n: int, f: int) -> int:
     return int(_lib.engram_ffn_workspace_bytes(ctx, n, f))
 
 
-def engram_ffn(ctx, x, x_scale, n, f, act, Wgu, gu_scale, Wd, res, y, gu, workspace, workspace_bytes, stream=None):
+def engram_ffn(ctx, x, x_scale, n, f, act, Wgu, gu_scale, Wd, res, y, saved, workspace, workspace_bytes, stream=None):
     _check(_lib.engram_ffn(ctx, _ptr(x), _ptr(x_scale), n, f, act, _ptr(Wgu), _ptr(gu_scale), _ptr(Wd), _ptr(res),
-                           _ptr(y), _ptr(gu), _ptr(workspace), workspace_bytes, _stream(stream)), "engram_ffn")
+                           _ptr(y), _ptr(saved), _ptr(workspace), workspace_bytes, _stream(stream)), "engram_ffn")
+
+
+def engram_ffn_saved_bytes(ctx, n: int, f: int) -> int:
+    return int(_lib.engram_ffn_saved_bytes(ctx, n, f))
 
 
 def engram_ffn_grad_workspace_bytes(ctx, n: int, f: int) -> int:
     return int(_lib.engram_ffn_grad_workspace_bytes(ctx, n, f))
 
 
-def engram_ffn_grad(ctx, d_y, x, gu, n, f, act, Wgu, Wd, d_x, d_Wgu, d_Wd, workspace, workspace_bytes, stream=None):
-    _check(_lib.engram_ffn_grad(ctx, _ptr(d_y), _ptr(x), _ptr(gu), n, f, act, _ptr(Wgu), _ptr(Wd), _ptr(d_x),
+def engram_ffn_grad(ctx, d_y, x, saved, n, f, act, Wgu, Wd, d_x, d_Wgu, d_Wd, workspace, workspace_bytes, stream=None):
+    _check(_lib.engram_ffn_grad(ctx, _ptr(d_y), _ptr(x), _ptr(saved), n, f, act, _ptr(Wgu), _ptr(Wd), _ptr(d_x),
                                 _ptr(d_Wgu), _ptr(d_Wd), _ptr(workspace), workspace_bytes, _stream(stream)),
            "engram_ffn_grad")
 

@@ -13,7 +13,7 @@
 //              accumulator; the activation and the product in the epilogue, so
 //              g and u reach global memory only when the backward needs them
 //   EPI_DGLU   da in the accumulator; the epilogue reads g and u and writes
-//              dg, du and a
+//              dg and du
 //   EPI_OUT    bf16 output, residual added in fp32 before the one rounding
 //   EPI_PART   fp32 partial sums of a split contraction (few rows: the
 //              weights are read once, by all SMs), joined by a second kernel
@@ -49,18 +49,19 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;
 
-template <bool PAIR>
-struct Geo {
-    static constexpr int B_BYTES = (PAIR ? MAX_BN / 2 : MAX_BN) * ROWB;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = PAIR ? 6 : 4;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 1024;   // tiles | barriers | alignment
-};
+// Shared memory: a ring of stages, each A rows then B rows of 128 bytes.  Few
+// rows stage only the rows they have, and a narrow tile only its columns, so
+// that more stages are in flight: the ring's round trip (free slot -> load ->
+// MMA -> free slot) is 1.4 us for one CTA and 2 us for a pair, and a stage
+// takes that over the number of stages at least.
+constexpr int TILE_AREA = 7 * 32768;    // seven stages of a 256 x 256 pair tile
+constexpr int MAX_STAGES = 14;
+constexpr int SMEM_BYTES = TILE_AREA + 1024 + 1024;   // ring | barriers | alignment
 
 struct __align__(8) Barriers {
-    uint64_t full[8];
-    uint64_t empty[8];
-    uint64_t pfull[8];    // PAIR, leader: the peer's stage is full
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
+    uint64_t pfull[MAX_STAGES];    // PAIR, leader: the peer's stage is full
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -77,11 +78,13 @@ struct FfnParams {
     int bn;                     // accumulator columns per tile (EPI_GLU: gate and up together)
     int n_tiles, m_units, splits, raster;
     uint32_t idesc;
+    int a_bytes, b_bytes;       // of a stage
+    int stages;
     int b_rows;                 // K-major B: rows per box
     int act;
     __nv_bfloat16* out;         // GLU: a [M][N]; DGLU: dgu [M][2N]; OUT: [M][N]
-    __nv_bfloat16* a_out;       // DGLU: a [M][N]
-    __nv_bfloat16* gu;          // GLU: [M][2N] or null; DGLU: input
+    uint4* gu_hi;               // upper 16 bits of g and u, 8 columns an element: written by GLU (or null), read by DGLU
+    uint2* gu_lo;               // the next 8 bits
     const __nv_bfloat16* res;   // OUT: [M][N] or null
     const float* row_scale;     // FP8: [M]
     const float* col_scale;     // FP8: [2N]
@@ -158,12 +161,58 @@ __device__ __forceinline__ float act_d(float g, float p, int act) {
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) { Vec<__nv_bfloat16>::load(p, f); }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) { Vec<__nv_bfloat16>::store(p, f); }
 
-// Eight columns from c of one row, whatever the accumulator's sums came from.
+// g and u are kept for the backward as 24 of their 32 bits (half a step 2^-16):
+// in bf16 their rounding would reach d_x and d_Wgu beside that of dg and du
+// (measured against 64 bits: 3.5e-3 of the norm, with 24 bits 2.4e-3); the
+// lower plane costs a byte per value.  Both planes are blocked as the
+// epilogues hold them, [row / 32][column / 8][row % 32] elements of 8 columns:
+// a warp's access is contiguous, where rows of 2 N would touch 32 lines
+// (d_gate_up of 16372 rows, d 2560, f 6824: 1343 us by rows, 673 us blocked).
+__device__ __forceinline__ int64_t at24(const FfnParams& p, int64_t row, int col) {
+    return ((row >> 5) * (p.N / 4) + col / 8) * 32 + (row & 31);
+}
+
+__device__ __forceinline__ uint32_t round24(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return (b & 0x7fffffffu) > 0x7f800000u ? 0x7fc00000u : b + 0x80u;   // NaN stays NaN
+}
+
+__device__ __forceinline__ void put24(const FfnParams& p, int64_t at, const float* f) {
+    uint32_t b[8], hi[4], lo[2];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = round24(f[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) hi[k] = __byte_perm(b[2 * k], b[2 * k + 1], 0x7632);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        lo[k] = __byte_perm(__byte_perm(b[4 * k], b[4 * k + 1], 0x0051), __byte_perm(b[4 * k + 2], b[4 * k + 3], 0x0051), 0x5410);
+    p.gu_hi[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    p.gu_lo[at] = make_uint2(lo[0], lo[1]);
+}
+
+struct Raw24 {
+    uint4 hi;
+    uint2 lo;
+    __device__ __forceinline__ void load(const FfnParams& p, int64_t at) {
+        hi = __ldg(p.gu_hi + at);
+        lo = __ldg(p.gu_lo + at);
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            // bytes: the high half of h[k / 2] or its low half, then byte k % 4 of the lower plane
+            const uint32_t top = k & 1 ? h[k / 2] & 0xffff0000u : h[k / 2] << 16;
+            f[k] = __uint_as_float(top | ((l[k / 4] >> (8 * (k & 3))) & 0xffu) << 8);
+        }
+    }
+};
+
+// Eight columns from c of one row, wherever the sums came from.
 __device__ __forceinline__ void put_glu8(const FfnParams& p, int64_t row, int c, float* g, float* u) {
-    if (p.gu) {
-        // the backward reads g and u rounded to bf16
-        store8(p.gu + row * 2 * p.N + c, g);
-        store8(p.gu + row * 2 * p.N + p.N + c, u);
+    if (p.gu_hi) {
+        put24(p, at24(p, row, c), g);
+        put24(p, at24(p, row, p.N + c), u);
     }
     float a[8];
 #pragma unroll
@@ -171,21 +220,19 @@ __device__ __forceinline__ void put_glu8(const FfnParams& p, int64_t row, int c,
     store8(p.out + row * p.N + c, a);
 }
 
-__device__ __forceinline__ void put_dglu8(const FfnParams& p, int64_t row, int c, const float* da) {
-    float g[8], u[8], dg[8], du[8], a[8];
-    load8(p.gu + row * 2 * p.N + c, g);
-    load8(p.gu + row * 2 * p.N + p.N + c, u);
+__device__ __forceinline__ void put_dglu8(const FfnParams& p, int64_t row, int c, const float* da, const Raw24& rg,
+                                          const Raw24& ru) {
+    float g[8], u[8], dg[8], du[8];
+    rg.get(g);
+    ru.get(u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float pr = act_p(g[k], p.act);
-        const float h = g[k] * pr;
-        a[k] = h * u[k];
-        du[k] = da[k] * h;
+        du[k] = da[k] * (g[k] * pr);
         dg[k] = da[k] * u[k] * act_d(g[k], pr, p.act);
     }
     store8(p.out + row * 2 * p.N + c, dg);
     store8(p.out + row * 2 * p.N + p.N + c, du);
-    store8(p.a_out + row * p.N + c, a);
 }
 
 __device__ __forceinline__ void put_out8(const FfnParams& p, int64_t row, int c, float* v) {
@@ -205,15 +252,15 @@ __device__ __forceinline__ void put_out8(const FfnParams& p, int64_t row, int c,
 template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
 __global__ void __launch_bounds__(THREADS, 1)
 ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
-    using GE = Geo<PAIR>;
     constexpr int NCTA = PAIR ? 2 : 1;
-    constexpr int STAGES = GE::STAGES;
+    const int STAGES = p.stages;
+    const int stage_bytes = p.a_bytes + p.b_bytes;
     constexpr int KSTEP = F8 ? 128 : 64;        // contraction indices per stage
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     const uint32_t tiles_u32 = smem_u32(smem);
-    Barriers* sb = reinterpret_cast<Barriers*>(smem + STAGES * GE::STAGE_BYTES);
+    Barriers* sb = reinterpret_cast<Barriers*>(smem + TILE_AREA);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0u;
     const bool leader = rank == 0;
@@ -259,6 +306,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = sb->tmem_base;
+    grid_dep_launch_dependents();
 
     // unit -> split, row unit and column tile; groups of `raster` row units
     // share the columns' slice of B while it is in L2
@@ -281,53 +329,77 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     if (warp == 0) {
         // ---------------- TMA producer
         if (lane == 0) {
-            int it = 0;
+            // A may come from a kernel of this call that is still running, B
+            // (weights, x, the saved a) never does: the first stages' B loads go
+            // out before the wait.
+            int it = 0, s = 0;
+            uint32_t ph = 0;
+            int early = 0;      // stages whose barrier is armed and whose B load is out
+            const bool remote = PAIR && !leader;
+            auto bar_of = [&](int st) { return remote ? peer_addr(&sb->pfull[st], 0u) : smem_u32(&sb->full[st]); };
+            auto load = [&](const CUtensorMap* m, int st, uint32_t dst, int x, int y) {
+                if (remote) tma_load_2d_peer_bar(m, dst, bar_of(st), x, y);
+                else tma_load_2d(m, dst, &sb->full[st], x, y);
+            };
+            auto arm = [&](int st) {
+                if (remote) mbar_arrive_expect_tx_remote(bar_of(st), (uint32_t)stage_bytes);
+                else mbar_arrive_expect_tx(&sb->full[st], (uint32_t)stage_bytes);
+            };
+            auto load_b = [&](int st, int nt, int k0) {
+                const uint32_t b_dst = tiles_u32 + st * stage_bytes + p.a_bytes;
+                if constexpr (BMN) {
+                    const int n0 = nt * p.bn + (int)rank * (p.bn / 2);
+                    const int cols = PAIR ? p.bn / 2 : p.bn;
+                    for (int c = 0; c < cols; c += 64) load(&map_b, st, b_dst + c * ROWB, n0 + c, k0);
+                } else if constexpr (GLU) {
+                    // gate rows from nt * bn / 2, up rows N behind; a pair's second CTA stages the up rows
+                    const int n0 = nt * (p.bn / 2);
+                    load(&map_b, st, b_dst, k0, n0 + (PAIR ? (int)rank * p.N : 0));
+                    if (!PAIR) load(&map_b, st, b_dst + p.b_rows * ROWB, k0, n0 + p.N);
+                } else {
+                    load(&map_b, st, b_dst, k0, nt * p.bn + (int)rank * (p.bn / 2));
+                }
+            };
+            if (unit0 < num_units) {
+                const Where w = where(unit0);
+                const int klo = k_lo(w.split);
+                early = min(STAGES, k_lo(w.split + 1) - klo);
+                for (int e = 0; e < early; ++e) {
+                    arm(e);
+                    load_b(e, w.nt, (klo + e) * KSTEP);
+                    sb->issued = e + 1;
+                }
+            }
+            grid_dep_wait();
             for (int u = unit0; u < num_units && !sb->abort_flag; u += step) {
                 const Where w = where(u);
                 const int m0 = (w.row * NCTA + (int)rank) * BM;
                 const int kend = k_lo(w.split + 1);
-                // first column (row of B) this CTA stages, and the second slice of GLU on one CTA
-                int n0, n1 = 0;
-                if (GLU) {
-                    n0 = w.nt * (p.bn / 2) + (PAIR ? (int)rank * p.N : 0);
-                    n1 = w.nt * (p.bn / 2) + p.N;
-                } else {
-                    n0 = w.nt * p.bn + (int)rank * (p.bn / 2);
-                }
-                const int bytes = A_BYTES + (PAIR ? p.bn / 2 : p.bn) * ROWB;
                 bool ok = true;
                 for (int kb = k_lo(w.split); kb < kend; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
-                    if (!wait_bounded<PAIR>(&sb->empty[s], ph ^ 1u, sb, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t a_dst = tiles_u32 + s * GE::STAGE_BYTES;
-                    const uint32_t b_dst = a_dst + A_BYTES;
-                    const bool remote = PAIR && !leader;
-                    const uint32_t bar = remote ? peer_addr(&sb->pfull[s], 0u) : smem_u32(&sb->full[s]);
-                    auto load = [&](const CUtensorMap* m, uint32_t dst, int x, int y) {
-                        if (remote) tma_load_2d_peer_bar(m, dst, bar, x, y);
-                        else tma_load_2d(m, dst, &sb->full[s], x, y);
-                    };
-                    if (remote) mbar_arrive_expect_tx_remote(bar, bytes);
-                    else mbar_arrive_expect_tx(&sb->full[s], bytes);
                     const int k0 = kb * KSTEP;
+                    if (it >= early) {
+                        if (!wait_bounded<PAIR>(&sb->empty[s], ph ^ 1u, sb, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        arm(s);
+                    }
+                    const uint32_t a_dst = tiles_u32 + s * stage_bytes;
                     if constexpr (AMN) {
-                        load(&map_a, a_dst, m0, k0);
-                        load(&map_a, a_dst + BK * ROWB, m0 + 64, k0);
+                        load(&map_a, s, a_dst, m0, k0);
+                        load(&map_a, s, a_dst + BK * ROWB, m0 + 64, k0);
                     } else {
-                        load(&map_a, a_dst, k0, m0);
+                        load(&map_a, s, a_dst, k0, m0);
                     }
-                    if constexpr (BMN) {
-                        const int cols = PAIR ? p.bn / 2 : p.bn;
-                        for (int c = 0; c < cols; c += 64) load(&map_b, b_dst + c * ROWB, n0 + c, k0);
-                    } else {
-                        load(&map_b, b_dst, k0, n0);
-                        if (GLU && !PAIR) load(&map_b, b_dst + p.b_rows * ROWB, k0, n1);
+                    if (it >= early) {
+                        load_b(s, w.nt, k0);
+                        sb->issued = it + 1;
                     }
-                    sb->issued = it + 1;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
                 if (!ok) break;
             }
@@ -335,7 +407,8 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     } else if (warp == 1 && (!PAIR || leader)) {
         // ---------------- MMA issuer
         if (lane == 0) {
-            int it = 0, tc = 0;
+            int it = 0, tc = 0, s = 0;
+            uint32_t ph = 0;
             for (int u = unit0; u < num_units && !sb->abort_flag; u += step, ++tc) {
                 const Where w = where(u);
                 const int acc = tc & 1;
@@ -346,17 +419,15 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 const int klo = k_lo(w.split), kend = k_lo(w.split + 1);
                 bool ok = true;
                 for (int kb = klo; kb < kend; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
                     if (!wait_bounded<PAIR>(&sb->full[s], ph, sb, p.status) ||
                         (PAIR && !wait_bounded<PAIR>(&sb->pfull[s], ph, sb, p.status))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = tiles_u32 + s * GE::STAGE_BYTES;
+                    const uint32_t a_addr = tiles_u32 + s * stage_bytes;
                     const uint64_t da = AMN ? smem_desc_mn(a_addr) : smem_desc_sw128(a_addr);
-                    const uint64_t db = BMN ? smem_desc_mn(a_addr + A_BYTES) : smem_desc_sw128(a_addr + A_BYTES);
+                    const uint64_t db = BMN ? smem_desc_mn(a_addr + p.a_bytes) : smem_desc_sw128(a_addr + p.a_bytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         // 16 contraction indices: 32 bytes inside the swizzled row, or 16 rows of 128 bytes
@@ -366,6 +437,10 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if constexpr (PAIR) umma_commit_pair_both(&sb->empty[s]);
                     else umma_commit(&sb->empty[s]);
                     sb->consumed = it + 1;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
                 if (!ok) break;
                 if constexpr (PAIR) umma_commit_pair_both(&sb->tfull[acc]);
@@ -377,18 +452,33 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t leader_tempty[2] = {PAIR ? peer_addr(&sb->tempty[0], 0u) : 0u, PAIR ? peer_addr(&sb->tempty[1], 0u) : 0u};
         int tc = 0;
+        grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
         for (int u = unit0; u < num_units; u += step, ++tc) {
             const Where w = where(u);
             const int acc = tc & 1;
             const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
-            const bool ok = wait_bounded<PAIR>(&sb->tfull[acc], aph, sb, p.status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
             const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
             const bool live = row < p.M;
             const int width = GLU ? p.bn / 2 : p.bn;       // output columns of the tile
             const int c_tile = w.nt * width;
+            // g and u of the next 16 columns are loaded while the current ones are worked on, the tile's
+            // first ones while its MMAs run
+            Raw24 rg[2], ru[2];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = c_tile + c + h * 8;
+                    if (live && c + h * 8 < width && col < p.N) {
+                        rg[h].load(p, at24(p, row, col));
+                        ru[h].load(p, at24(p, row, p.N + col));
+                    }
+                }
+            };
+            if constexpr (EPI == EPI_DGLU) fetch(half * 16);
+            const bool ok = wait_bounded<PAIR>(&sb->tfull[acc], aph, sb, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
             float rs = 1.f;
             if (F8 && live) rs = __ldg(p.row_scale + row);
 #pragma unroll 1
@@ -396,6 +486,15 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 uint32_t x[16], y[16];
                 tmem_ld16(taddr + c, x);
                 if (GLU) tmem_ld16(taddr + width + c, y);
+                Raw24 cg[2], cu[2];
+                if constexpr (EPI == EPI_DGLU) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        cg[h] = rg[h];
+                        cu[h] = ru[h];
+                    }
+                    if (c + 32 < width) fetch(c + 32);
+                }
                 tmem_wait_ld(x);
                 if (GLU) tmem_wait_ld(y);
 #pragma unroll
@@ -416,7 +515,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         }
                     }
                     if constexpr (EPI == EPI_GLU) put_glu8(p, row, col, f, g);
-                    if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, col, f);
+                    if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, col, f, cg[h], cu[h]);
                     if constexpr (EPI == EPI_OUT) put_out8(p, row, col, f);
                     if constexpr (EPI == EPI_PART) {
                         const int64_t ld = GLU ? 2 * (int64_t)p.N : p.N;
@@ -489,12 +588,14 @@ __global__ void ffn_join_kernel(const FfnParams p) {
     const int vec = p.N / 8;
     const int64_t total = (int64_t)p.M * vec;
     const int64_t ld = EPI == EPI_GLU ? 2 * (int64_t)p.N : p.N;
+    grid_dep_wait();
+    grid_dep_launch_dependents();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / vec;
         const int c = (int)(i - row * vec) * 8;
         float f[8] = {}, g[8] = {};
         auto add = [&](float* acc, const float* from) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(from)), b = __ldg(reinterpret_cast<const float4*>(from) + 1);
+            const float4 a = *reinterpret_cast<const float4*>(from), b = *(reinterpret_cast<const float4*>(from) + 1);
             acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
             acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
         };
@@ -505,7 +606,12 @@ __global__ void ffn_join_kernel(const FfnParams p) {
             if (EPI == EPI_GLU) add(g, from + p.N);
         }
         if constexpr (EPI == EPI_GLU) put_glu8(p, row, c, f, g);
-        if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, c, f);
+        if constexpr (EPI == EPI_DGLU) {
+            Raw24 rg, ru;
+            rg.load(p, at24(p, row, c));
+            ru.load(p, at24(p, row, p.N + c));
+            put_dglu8(p, row, c, f, rg, ru);
+        }
         if constexpr (EPI == EPI_OUT) put_out8(p, row, c, f);
     }
 }
@@ -518,36 +624,44 @@ bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
 }
 
 // How a product is cut: one CTA or a pair per tile, accumulator columns,
-// splits of the contraction.
+// splits of the contraction, bytes and number of the stages.
 struct Plan {
     bool pair;
-    int bn, m_units, n_tiles, kb, splits;
+    int bn, m_units, n_tiles, kb, splits, a_bytes, b_bytes, stages;
     size_t part_bytes;
 };
 
-// M x N outputs (N: channels of GLU) over a contraction of kb stages.
-Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool bmn) {
+// M x N outputs (N: channels of GLU) over a contraction of kb stages: the cut
+// with the least time by these rates (us; measured, see the header):
+//   a stage   the larger of its MMAs, the ring's round trip over its stages,
+//             and its bytes into one SM
+//   all       the weights from HBM
+//   a split   the partial sums written and read back, and the join's launch
+Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
     Plan best{};
     double best_cost = 1e30;
     const bool pair = M > BM;
     const int workers = pair ? c->num_sms / 2 : c->num_sms;
     const int64_t cols = glu ? 2 * N : N;
-    const int step = bmn ? (pair ? 128 : 64) : 32;
+    const int step = bmn ? (pair ? 128 : 64) : (pair ? 32 : 16);
+    const int a_rows = !pair && !amn ? (int)(M + 7) / 8 * 8 : BM;
+    const int64_t m_units = pair ? (M + 2 * BM - 1) / (2 * BM) : 1;
     for (int bn = MAX_BN; bn >= (bmn ? step : 64); bn -= step) {
         const int width = glu ? bn / 2 : bn;
-        const int64_t m_units = pair ? (M + 2 * BM - 1) / (2 * BM) : 1;
         const int64_t n_tiles = (N + width - 1) / width;
         const int64_t tiles = m_units * n_tiles;
+        const int a_bytes = a_rows * ROWB, b_bytes = (pair ? bn / 2 : bn) * ROWB;
+        // the MMA reads 128 rows of A whatever was staged: the last stage's lie inside the ring too
+        const int stages = std::min(MAX_STAGES, (TILE_AREA - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
+        const double stage = std::max(std::max(0.365 * bn / 256, (pair ? 2.0 : 1.4) / stages), (a_bytes + b_bytes) / 80e3);
         for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
             if (splits > 1 && tiles * (splits - 1) >= workers) break;
             const int64_t waves = (tiles * splits + workers - 1) / workers;
-            // stages in a row, each the larger of its MMAs (256 columns: 1) and its operand bytes
-            const double stage = std::max(bn / 256.0, (A_BYTES + (pair ? bn / 2 : bn) * ROWB) / 49152.0);
-            double cost = waves * ((kb + splits - 1) / splits) * stage;
-            if (splits > 1) cost += 6.0 + (double)splits * M * cols * 8 / (16e3 * 1e3);
-            if (cost < best_cost * 0.999) {
+            double cost = std::max(waves * ((kb + splits - 1) / splits) * stage, (double)kb * ROWB * cols / 6.4e6);
+            if (splits > 1) cost += 3.0 + (double)splits * M * cols * 8 / 6e6;
+            if (cost < best_cost * 0.98) {
                 best_cost = cost;
-                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits,
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages,
                             splits > 1 ? align256((size_t)splits * M * cols * 4) : 0};
             }
         }
@@ -556,18 +670,18 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
 }
 
 template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
-cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, cudaStream_t s) {
-    using GE = Geo<PAIR>;
+cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, bool pdl,
+                       cudaStream_t s) {
     auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8>;
     static std::mutex mu;
     static int max_units[64] = {};              // CTAs or pairs resident at once, per device
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = GE::SMEM_BYTES;
+    cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 0;
@@ -582,7 +696,7 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
     {
         std::lock_guard<std::mutex> lock(mu);
         if (max_units[dev] == 0) {
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM_BYTES);
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
             if (e != cudaSuccess) return e;
             int mc = num_sms;
             if (PAIR) {
@@ -599,17 +713,25 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
     const int64_t units = (int64_t)p.m_units * p.n_tiles * p.splits;
     if (units >= (int64_t)1 << 31) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) * std::min<int64_t>(units, cap)), 1, 1);
+    if (pdl) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
 }
 
+// after: the kernel before on the stream is one of this call's, so this one
+// may be its programmatic dependent (timed calls put events in between).
 // One product: A [M][K] (or [K][M] with AMN), B [N][K] (or [K][N] with BMN;
 // GLU: [2N][K]), and its epilogue, through partial sums when the plan splits.
 template <int EPI, bool AMN, bool BMN, bool F8 = false>
 cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int64_t N, int64_t K, FfnParams p, float* part,
-                    const char* name, cudaStream_t s) {
+                    const char* name, bool after, cudaStream_t s) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int kstep = F8 ? 128 : 64;
-    const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, BMN);
+    const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, AMN, BMN);
+    const bool pdl = after && !c->prof;
     p.M = (int)M;
     p.N = (int)N;
     p.kb = pl.kb;
@@ -617,6 +739,9 @@ cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int6
     p.n_tiles = pl.n_tiles;
     p.m_units = pl.m_units;
     p.splits = pl.splits;
+    p.a_bytes = pl.a_bytes;
+    p.b_bytes = pl.b_bytes;
+    p.stages = pl.stages;
     p.raster = 8;
     p.status = c->d_status;
     p.part = part;
@@ -626,34 +751,58 @@ cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int6
               ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((pl.pair ? 256 : 128) >> 4) << 24);
     CUtensorMap ma, mb;
     const int64_t b_cols = GLU ? 2 * N : N;
-    const bool ok = (AMN ? operand_map(&ma, A, K, M, BK, F8) : operand_map(&ma, A, M, K, BM, F8)) &&
+    const bool ok = (AMN ? operand_map(&ma, A, K, M, BK, F8) : operand_map(&ma, A, M, K, pl.a_bytes / ROWB, F8)) &&
                     (BMN ? operand_map(&mb, B, K, b_cols, BK, F8) : operand_map(&mb, B, b_cols, K, p.b_rows, F8));
     if (!ok) return cudaErrorInvalidValue;
     prof_begin(c, s, name);
     cudaError_t e;
     if (pl.splits == 1)
-        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, s)
-                    : launch_one<EPI, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, s);
+        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, pdl, s)
+                    : launch_one<EPI, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, pdl, s);
     else
-        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, s)
-                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, s);
+        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, pdl, s)
+                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, pdl, s);
     prof_end(c, s);
     if (e == cudaSuccess && pl.splits > 1) {
         prof_begin(c, s, "ffn_join");
         const int64_t threads = M * (N / 8);
         const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
-        ffn_join_kernel<EPI><<<blocks, 256, 0, s>>>(p);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(blocks, 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = c->prof ? 0 : 1;
+        e = cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI>, p);
         prof_end(c, s);
-        e = cudaGetLastError();
     }
     return e;
 }
 
-// Scratch: the products' shared partial sums, then the intermediate matrices.
+// What the forward keeps for the backward: the two planes of g and u, and
+// a = act(g) u as the down projection read it.
+struct Saved {
+    __nv_bfloat16* a;       // [n][f]
+    uint4* hi;              // [ceil(n / 32)][2f / 8][32]
+    uint2* lo;
+    size_t bytes;
+};
+
+Saved saved_of(const void* base, int64_t n, int64_t f) {
+    char* p = static_cast<char*>(const_cast<void*>(base));
+    const int64_t elems = (n + 31) / 32 * 32 * (f / 4);
+    return Saved{reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<uint4*>(p + n * f * 2),
+                 reinterpret_cast<uint2*>(p + n * f * 2 + elems * 16), (size_t)(n * f * 2 + elems * 24)};
+}
+
+// Scratch: the products' shared partial sums, then the intermediate matrix
+// (forward: a [n][f], unless it is saved; backward: dg and du [n][2f]).
 struct FfnWs {
     float* part;
-    __nv_bfloat16* a;       // [n][f]
-    __nv_bfloat16* dgu;     // [n][2f], backward
+    __nv_bfloat16* mid;
     size_t bytes;
 };
 
@@ -662,14 +811,14 @@ FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad
     auto kb = [](int64_t K) { return (int)((K + 63) / 64); };
     size_t part = 0;
     if (grad) {
-        part = std::max(part, make_plan(c, n, f, kb(d), false, true).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, true).part_bytes);
-        part = std::max(part, make_plan(c, d, f, kb(n), false, true).part_bytes);
-        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, true).part_bytes);
+        part = std::max(part, make_plan(c, n, f, kb(d), false, false, true).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, false, true).part_bytes);
+        part = std::max(part, make_plan(c, d, f, kb(n), false, true, true).part_bytes);
+        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, true, true).part_bytes);
     } else {
         const bool f8 = c->cfg.dtype == ENGRAM_FP8;
-        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(f), false, false).part_bytes);
+        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false, false).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(f), false, false, false).part_bytes);
     }
     FfnWs w{};
     char* p = static_cast<char*>(base);
@@ -679,8 +828,7 @@ FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad
         return q;
     };
     w.part = reinterpret_cast<float*>(take(part));
-    w.a = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * f * 2));
-    if (grad) w.dgu = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * 2 * f * 2));
+    w.mid = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * f * (grad ? 4 : 2)));
     w.bytes = (size_t)(p - static_cast<char*>(base));
     return w;
 }
@@ -726,18 +874,18 @@ size_t engram_ffn_workspace_bytes(const engram_ctx* c, int64_t n, int32_t f) {
 }
 
 engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int64_t n, int32_t f, int32_t act,
-                         const void* Wgu, const float* gu_scale, const void* Wd, const void* res, void* y, void* gu,
+                         const void* Wgu, const float* gu_scale, const void* Wd, const void* res, void* y, void* saved,
                          void* workspace, size_t workspace_bytes, cudaStream_t s) {
     engram_status st = ffn_shape(c, n, f, act, false);
     if (st != ENGRAM_OK) return st;
     const bool f8 = c->cfg.dtype == ENGRAM_FP8;
-    if (f8 && gu) return inval("gu is for the backward, which takes bf16 contexts");
+    if (f8 && saved) return inval("saved is for the backward, which takes bf16 contexts");
     if (n == 0) return ENGRAM_OK;
     if (!x || !Wgu || !Wd || !y) return inval("null tensor pointer");
     if (f8 ? (!x_scale || !gu_scale) : (x_scale || gu_scale))
         return inval("x_scale and gu_scale go with ENGRAM_FP8, and are required there");
-    if (!aligned16(x) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(res) || !aligned16(y) || !aligned16(gu))
-        return inval("x, Wgu, Wd, res, y and gu must be 16-byte aligned");
+    if (!aligned16(x) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(res) || !aligned16(y) || !aligned16(saved))
+        return inval("x, Wgu, Wd, res, y and saved must be 16-byte aligned");
     const FfnWs w = ffn_carve(c, workspace, n, f, false);
     st = check_ws(workspace, workspace_bytes, w.bytes);
     if (st == ENGRAM_OK) st = check_device(c);
@@ -746,17 +894,22 @@ engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int
     const int64_t d = c->cfg.hidden;
     FfnParams p{};
     p.act = act;
-    p.out = w.a;
-    p.gu = static_cast<__nv_bfloat16*>(gu);
+    p.out = w.mid;
+    if (saved) {
+        const Saved sv = saved_of(saved, n, f);
+        p.out = sv.a;
+        p.gu_hi = sv.hi;
+        p.gu_lo = sv.lo;
+    }
     p.row_scale = x_scale;
     p.col_scale = gu_scale;
-    cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up_fp8", s)
-                       : product<EPI_GLU, false, false>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up", s);
+    cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up_fp8", false, s)
+                       : product<EPI_GLU, false, false>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up", false, s);
     if (e != cudaSuccess) return cuda_fail("feed-forward gate/up launch", e);
     FfnParams o{};
     o.out = static_cast<__nv_bfloat16*>(y);
     o.res = static_cast<const __nv_bfloat16*>(res);
-    e = product<EPI_OUT, false, false>(c, w.a, Wd, n, d, f, o, w.part, "ffn_down", s);
+    e = product<EPI_OUT, false, false>(c, p.out, Wd, n, d, f, o, w.part, "ffn_down", true, s);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward down launch", e);
 }
 
@@ -765,14 +918,19 @@ size_t engram_ffn_grad_workspace_bytes(const engram_ctx* c, int64_t n, int32_t f
     return ffn_carve(c, nullptr, std::max<int64_t>(1, n), f, true).bytes;
 }
 
-engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, const void* gu, int64_t n, int32_t f,
+size_t engram_ffn_saved_bytes(const engram_ctx* c, int64_t n, int32_t f) {
+    if (ffn_shape(c, n, f, ENGRAM_ACT_SILU, true) != ENGRAM_OK) return 0;
+    return saved_of(nullptr, n, f).bytes;
+}
+
+engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, const void* saved, int64_t n, int32_t f,
                               int32_t act, const void* Wgu, const void* Wd, void* d_x, void* d_Wgu, void* d_Wd,
                               void* workspace, size_t workspace_bytes, cudaStream_t s) {
     engram_status st = ffn_shape(c, n, f, act, true);
     if (st != ENGRAM_OK) return st;
     if (!d_Wgu || !d_Wd) return inval("null weight gradient");
-    if (n > 0 && (!d_y || !x || !gu || !Wgu || !Wd || !d_x)) return inval("null tensor pointer");
-    if (!aligned16(d_y) || !aligned16(x) || !aligned16(gu) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(d_x) ||
+    if (n > 0 && (!d_y || !x || !saved || !Wgu || !Wd || !d_x)) return inval("null tensor pointer");
+    if (!aligned16(d_y) || !aligned16(x) || !aligned16(saved) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(d_x) ||
         !aligned16(d_Wgu) || !aligned16(d_Wd))
         return inval("tensors must be 16-byte aligned");
     FfnWs w{};
@@ -792,22 +950,23 @@ engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, con
     }
     FfnParams p{};
     p.act = act;
-    p.out = w.dgu;
-    p.a_out = w.a;
-    p.gu = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(gu));
-    cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, Wd, n, f, d, p, w.part, "ffn_d_gate_up", s);
+    const Saved sv = saved_of(saved, n, f);
+    p.out = w.mid;
+    p.gu_hi = sv.hi;
+    p.gu_lo = sv.lo;
+    cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, Wd, n, f, d, p, w.part, "ffn_d_gate_up", false, s);
     FfnParams o{};
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_x);
-        e = product<EPI_OUT, false, true>(c, w.dgu, Wgu, n, d, 2 * (int64_t)f, o, w.part, "ffn_d_x", s);
+        e = product<EPI_OUT, false, true>(c, w.mid, Wgu, n, d, 2 * (int64_t)f, o, w.part, "ffn_d_x", true, s);
     }
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_Wgu);
-        e = product<EPI_OUT, true, true>(c, w.dgu, x, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", s);
+        e = product<EPI_OUT, true, true>(c, w.mid, x, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", true, s);
     }
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_Wd);
-        e = product<EPI_OUT, true, true>(c, d_y, w.a, d, f, n, o, w.part, "ffn_d_Wd", s);
+        e = product<EPI_OUT, true, true>(c, d_y, sv.a, d, f, n, o, w.part, "ffn_d_Wd", true, s);
     }
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward backward launches", e);
 }

@@ -523,17 +523,19 @@ ENGRAM_API engram_status engram_add_norm_grad(engram_ctx* ctx, const void* d_y, 
  *        one is stored);
  *   res  [n][d] bf16 or null, added in fp32 before y's one rounding;
  *   y    [n][d] bf16; may be res or x;
- *   gu   [n][2f] bf16 or null: g and u, for the backward (bf16 contexts).
+ *   saved  null, or engram_ffn_saved_bytes(ctx, n, f) bytes for the
+ *        backward (bf16 contexts): act(g) * u in bf16, and g and u with 24 of
+ *        their 32 bits.
  * f is a multiple of 8, all tensors 16-byte aligned.  Scratch:
  * engram_ffn_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
  *
  * engram_ffn_grad, from the gradient d_y of y (that of res is d_y itself) and
- * the forward's x and gu:
+ * the forward's x and saved:
  *   da = d_y Wd, dg = da * u * act'(g), du = da * act(g);
  *   d_x [n][d] = [dg du] Wgu, d_Wgu [2f][d] = [dg du]^T x,
  *   d_Wd [d][f] = d_y^T (act(g) * u),
- * all bf16, each sum in fp32 and rounded once when stored (dg, du and
- * act(g) * u are held in bf16 between the products); d_Wgu and d_Wd are
+ * all bf16, each sum in fp32 and rounded once when stored (dg and du are held
+ * in bf16 between the products, act(g) * u is the saved one); d_Wgu and d_Wd are
  * overwritten.  d_x must not overlap the inputs.  ENGRAM_BF16 contexts only.
  * Scratch: engram_ffn_grad_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
  *
@@ -543,10 +545,11 @@ typedef enum engram_act { ENGRAM_ACT_SILU = 0, ENGRAM_ACT_GELU = 1 } engram_act;
 ENGRAM_API size_t engram_ffn_workspace_bytes(const engram_ctx* ctx, int64_t n, int32_t f);
 ENGRAM_API engram_status engram_ffn(engram_ctx* ctx, const void* x, const float* x_scale, int64_t n, int32_t f,
                                     int32_t act, const void* Wgu, const float* gu_scale, const void* Wd,
-                                    const void* res, void* y, void* gu, void* workspace, size_t workspace_bytes,
-                                    cudaStream_t stream);
+                                    const void* res, void* y, void* saved, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+ENGRAM_API size_t engram_ffn_saved_bytes(const engram_ctx* ctx, int64_t n, int32_t f);
 ENGRAM_API size_t engram_ffn_grad_workspace_bytes(const engram_ctx* ctx, int64_t n, int32_t f);
-ENGRAM_API engram_status engram_ffn_grad(engram_ctx* ctx, const void* d_y, const void* x, const void* gu, int64_t n,
+ENGRAM_API engram_status engram_ffn_grad(engram_ctx* ctx, const void* d_y, const void* x, const void* saved, int64_t n,
                                          int32_t f, int32_t act, const void* Wgu, const void* Wd, void* d_x,
                                          void* d_Wgu, void* d_Wd, void* workspace, size_t workspace_bytes,
                                          cudaStream_t stream);

@@ -8,7 +8,8 @@ Tolerances, with m = 2^-8 (half a bf16 step, torch.finfo(bfloat16).eps / 2):
   carries 2^-24 |k| and __expf 2 + 1.2 |k| ulp, so at |k| <= 40 (beyond, p is
   0 or 1 to fp32) p is within 2^-17 relative; act' within 2^-15 absolute
   (its terms are at most 2 in magnitude);
-  each value stored in bf16 adds m of it.  |act'| <= 1.13.
+  each value stored in bf16 adds m of it, g and u saved with 24 bits (15 of
+  the mantissa stored, a step of 2^-15 relative) half a step, 2^-16 of theirs.  |act'| <= 1.13.
 The bounds are carried through the products with magnitudes."""
 
 import numpy as np
@@ -38,16 +39,31 @@ def inputs(n, d, f, seed=1):
     return x, Wgu, Wd
 
 
-def check_forward(y, gu, x, Wgu, Wd, kind, res=None):
+def planes(saved, n, f):
+    """(g and u [n][2f] fp32, a [n][f] bf16) of what the forward saves: a, then two planes of 8-column elements
+    blocked [row / 32][column / 8][row % 32]"""
+    rb, cut = (n + 31) // 32, n * f * 2
+    elems = rb * 32 * (f // 4)
+    shape = (rb, f // 4, 32, 8)
+    hi = saved[cut:cut + elems * 16].view(torch.int16).view(shape).to(torch.int32) << 16
+    lo = saved[cut + elems * 16:].view(shape).to(torch.int32) << 8
+    gu = (hi | lo).permute(0, 2, 1, 3).reshape(rb * 32, 2 * f)[:n].contiguous().view(torch.float32)
+    return gu, saved[:cut].view(torch.bfloat16).view(n, f)
+
+
+def check_forward(y, saved, x, Wgu, Wd, kind, res=None):
     """x, Wgu, Wd, res in fp64"""
     f, d = Wd.shape[1], Wd.shape[0]
     want, guw = R.ffn(x, Wgu, Wd, kind, res)
     e_gu = d * A23 * (np.abs(x) @ np.abs(Wgu).T)
-    if gu is not None:
-        assert (np.abs(f64(gu) - guw) <= M * np.abs(guw) + (1 + M) * e_gu).all()
+    if saved is not None:
+        gu = planes(saved, x.shape[0], f)[0]
+        assert (np.abs(f64(gu) - guw) <= 2.0 ** -16 * np.abs(guw) + (1 + M) * e_gu).all()
     h, u = R.act(guw[:, :f], kind)[0], guw[:, f:]
     a = np.abs(h * u)
     e_a = (M + 2.0 ** -17) * a + 1.13 * e_gu[:, :f] * np.abs(u) + np.abs(h) * e_gu[:, f:]
+    if saved is not None:
+        assert (np.abs(f64(planes(saved, x.shape[0], f)[1]) - h * u) <= (1 + M) * e_a).all()
     bound = M * np.abs(want) + (1 + M) * (e_a + f * A23 * a) @ np.abs(Wd).T + 1e-6
     err = np.abs(f64(y) - want)
     assert (err <= bound).all(), (int((err > bound).sum()), float(err.max()))
@@ -63,10 +79,10 @@ def test_ffn(eb, n, d, f, kind, with_res):
     eng = engine(eb, d)
     x, Wgu, Wd = inputs(n, d, f)
     res = randn(9, n, d) if with_res else None
-    y, gu = eng.ffn(x, Wgu, Wd, act=kind, res=res, save=True)
+    y, saved = eng.ffn(x, Wgu, Wd, act=kind, res=res, save=True)
     assert eng.status() == (eb.ENGRAM_OK, 0)
-    check_forward(y, gu, f64(x), f64(Wgu), f64(Wd), kind, None if res is None else f64(res))
-    assert torch.equal(eng.ffn(x, Wgu, Wd, act=kind, res=res), y)       # the same bits without gu
+    check_forward(y, saved, f64(x), f64(Wgu), f64(Wd), kind, None if res is None else f64(res))
+    assert torch.equal(eng.ffn(x, Wgu, Wd, act=kind, res=res), y)       # the same bits without saving
 
 
 @pytest.mark.parametrize("n,d,f", [(1, 128, 8), (7, 128, 200), (129, 256, 136), (300, 2560, 264), (1000, 640, 392)])
@@ -87,11 +103,11 @@ def test_ffn_fp8(eb, n, d, f, kind):
 def test_ffn_grad(eb, n, d, f, kind):
     eng = engine(eb, d)
     x, Wgu, Wd = inputs(n, d, f)
-    _, gu = eng.ffn(x, Wgu, Wd, act=kind, save=True)
+    _, saved = eng.ffn(x, Wgu, Wd, act=kind, save=True)
     d_y = randn(7, n, d, sd=0.5)
-    got = eng.ffn_grad(d_y, x, gu, Wgu, Wd, act=kind)
+    got = eng.ffn_grad(d_y, x, saved, Wgu, Wd, act=kind)
     assert eng.status() == (eb.ENGRAM_OK, 0)
-    X, W, D, G, dy = f64(x), f64(Wgu), f64(Wd), f64(gu), f64(d_y)
+    X, W, D, G, dy = f64(x), f64(Wgu), f64(Wd), f64(planes(saved, n, f)[0]), f64(d_y)
     want = R.ffn_grad(dy, X, G, W, D, kind)
     h, dh = R.act(G[:, :f], kind)
     u = G[:, f:]
@@ -108,7 +124,7 @@ def test_ffn_grad(eb, n, d, f, kind):
         err = np.abs(f64(g) - w)
         bound = M * np.abs(w) + (1 + M) * b + 1e-6
         assert (err <= bound).all(), (name, int((err > bound).sum()), float(err.max()))
-    again = eng.ffn_grad(d_y, x, gu, Wgu, Wd, act=kind)
+    again = eng.ffn_grad(d_y, x, saved, Wgu, Wd, act=kind)
     assert all(torch.equal(p, q) for p, q in zip(got, again))
 
 
@@ -130,12 +146,12 @@ def test_ffn_products_are_exact_on_small_integers(eb, n):
     up = lambda a: torch.from_numpy(a).to(torch.bfloat16).cuda()
     W = np.concatenate([Wg, Wu])
     g, u = x @ Wg.T, x @ Wu.T
-    y, gu = eng.ffn(up(x), up(W), up(Wd), save=True)
-    assert np.array_equal(f64(gu), np.concatenate([g, u], 1))
+    y, saved = eng.ffn(up(x), up(W), up(Wd), save=True)
+    assert np.array_equal(f64(planes(saved, n, f)[0]), np.concatenate([g, u], 1))
     a = g * u
     assert np.array_equal(f64(y), f64(up(a @ Wd.T)))
     dy = rng.integers(0, 2, (n, d)).astype(float)
-    d_x, d_Wgu, d_Wd = eng.ffn_grad(up(dy), up(x), gu, up(W), up(Wd))
+    d_x, d_Wgu, d_Wd = eng.ffn_grad(up(dy), up(x), saved, up(W), up(Wd))
     da = dy @ Wd
     dgu = f64(up(np.concatenate([da * u, da * g], 1)))    # act'(g) = 1; sums of two rounded to bf16 as stored
     assert np.array_equal(f64(d_x), f64(up(dgu @ W)))
@@ -153,9 +169,9 @@ def test_ffn_in_place_residual_and_no_rows(eb):
     eb.engram_ffn(eng.ctx, into, None, 130, 136, 0, Wgu, None, Wd, into, into, None, ws, need)
     assert torch.equal(into, y)
     none = torch.empty(0, 264, dtype=torch.bfloat16, device="cuda")
-    y0, gu0 = eng.ffn(none, Wgu, Wd, save=True)
-    assert y0.shape == (0, 264) and gu0.shape == (0, 272)
-    d_x, d_Wgu, d_Wd = eng.ffn_grad(y0, none, gu0, Wgu, Wd)
+    y0, saved0 = eng.ffn(none, Wgu, Wd, save=True)
+    assert y0.shape == (0, 264) and saved0.shape == (0,)
+    d_x, d_Wgu, d_Wd = eng.ffn_grad(y0, none, saved0, Wgu, Wd)
     assert d_x.shape == (0, 264) and not d_Wgu.any() and not d_Wd.any()
 
 
@@ -178,11 +194,11 @@ def test_ffn_refuses(eb):
     ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
     y, s = torch.empty_like(x), torch.ones(128, device="cuda")
 
-    def call(e=eng, n=4, f=64, act=0, x=x, xs=None, gs=None, gu=None, ws=ws, size=ws.numel()):
-        eb.engram_ffn(e.ctx, x, xs, n, f, act, Wgu, gs, Wd, None, y, gu, ws, size)
+    def call(e=eng, n=4, f=64, act=0, x=x, xs=None, gs=None, saved=None, ws=ws, size=ws.numel()):
+        eb.engram_ffn(e.ctx, x, xs, n, f, act, Wgu, gs, Wd, None, y, saved, ws, size)
 
     for kw in (dict(n=-1), dict(f=0), dict(f=12), dict(act=2), dict(x=None), dict(xs=s), dict(ws=ws[1:], size=ws.numel() - 1),
-               dict(ws=None), dict(x=x.view(-1)[1:]), dict(e=f8), dict(e=f8, xs=s, gs=s, gu=Wgu)):
+               dict(ws=None), dict(x=x.view(-1)[1:]), dict(e=f8), dict(e=f8, xs=s, gs=s, saved=Wgu)):
         with pytest.raises(eb.EngramError) as ei:
             call(**kw)
         assert ei.value.status == eb.ENGRAM_E_INVAL, kw

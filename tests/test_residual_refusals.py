@@ -57,7 +57,7 @@ TOK = torch.zeros(2, 5, dtype=torch.int32)
     (lambda e: e.ffn(bf(3, 16), bf(16, 16), bf(8, 16)), "Wgu"),
     (lambda e: e.ffn(bf(3, 16), bf(16, 16), bf(16, 8), res=bf(3, 8)), "res"),
     (lambda e: e.ffn(bf(3, 16), bf(16, 16), bf(16, 8), x_scale=torch.ones(3)), "FP8"),
-    (lambda e: e.ffn_grad(bf(3, 16), bf(3, 16), bf(3, 8), bf(16, 16), bf(16, 8)), "gu"),
+    (lambda e: e.ffn_grad(bf(3, 16), bf(3, 16), bf(3, 8), bf(16, 16), bf(16, 8)), "saved"),
     (lambda e: e.ffn_grad(bf(2, 16), bf(3, 16), bf(3, 16), bf(16, 16), bf(16, 8)), "d_y"),
 ])
 def test_methods_refuse_bad_tensors(eng, call, why):
@@ -75,5 +75,6 @@ def test_entry_points_refuse_a_null_context(eb):
     assert lib.engram_ffn(None, None, None, 1, 8, 0, None, None, None, None, None, None, None, 0, None) == inval
     assert lib.engram_ffn_grad(None, None, None, None, 1, 8, 0, None, None, None, None, None, None, 0, None) == inval
     assert eb.engram_ffn_workspace_bytes(None, 4, 8) == 0
+    assert eb.engram_ffn_saved_bytes(None, 4, 8) == 0
     assert eb.engram_embed_grad_workspace_bytes(None, 4) == 0
     assert eb.engram_add_norm_grad_workspace_bytes(None, 4) == 0
