@@ -21,8 +21,8 @@
 // in dx, both in the weight gradients) is loaded as it lies and multiplied
 // MN-major: nothing is transposed in memory.
 //
-// Persistent, warp-specialised (384 threads): warp 0 TMA producer, warp 1
-// allocates TMEM and issues tcgen05.mma, warps 4-11 epilogue (two warps per
+// Persistent, warp-specialised (416 threads): warps 0 and 2-4 TMA producers,
+// warp 1 allocates TMEM and issues tcgen05.mma, warps 5-12 epilogue (two warps per
 // TMEM lane quarter, taking turns on 16-column chunks).  Two accumulators of
 // up to 256 columns: the epilogue of a tile overlaps the MMAs of the next.
 // More than 128 rows run on CTA pairs (M = 256, each CTA stages its rows of A
@@ -46,7 +46,8 @@ constexpr int BK = 64;                  // contraction indices per stage of MN-m
 constexpr int A_BYTES = BM * ROWB;      // 16 KB
 constexpr int MAX_BN = 256;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 128 + EPI_WARPS * 32;
+constexpr int EPI_WARP0 = 5;            // warps 0-4: producers and MMA issuer
+constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int TMEM_COLS = 512;
 
 // Shared memory: a ring of stages, each A rows then B rows of 128 bytes.  Few
@@ -61,13 +62,12 @@ constexpr int SMEM_BYTES = TILE_AREA + 1024 + 1024;   // ring | barriers | align
 struct __align__(8) Barriers {
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
-    uint64_t pfull[MAX_STAGES];    // PAIR, leader: the peer's stage is full
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
     uint32_t tmem_base;
     volatile int abort_flag;
-    int issued;
+    int issued[5];            // stages loaded by each producer warp
     int consumed;
     uint32_t peer_abort;
 };
@@ -92,14 +92,15 @@ struct FfnParams {
     uint32_t* status;
 };
 
-template <bool CLUSTER>
+// Bounded wait for the phase with `parity`; false when the CTA aborted or the
+// wait ran out.  Operands arrive by the async proxy and accumulators are read
+// behind tcgen05 fences, so CTA scope serves the pair's barriers too.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Barriers* sb, uint32_t* status) {
     const uint32_t a = smem_u32(bar);
-    auto try_wait = [&]() { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
-    if (try_wait()) return true;
+    if (mbar_try_wait(a, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-        if (try_wait()) return true;
+        if (mbar_try_wait(a, parity)) return true;
         if (sb->abort_flag) return false;
         if (clock64() - t0 > kWaitCycles) {
             flag(status, ENGRAM_ERR_TIMEOUT);
@@ -270,9 +271,8 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&sb->full[s], 1);
+            mbar_init(&sb->full[s], (2 + AMN + BMN) * NCTA);   // the producers of each CTA, on the leader's barrier
             mbar_init(&sb->empty[s], 1);
-            mbar_init(&sb->pfull[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sb->tfull[a], 1);
@@ -280,7 +280,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         }
         mbar_init(&sb->drain, 1);
         sb->abort_flag = 0;
-        sb->issued = 0;
+        for (int w = 0; w < 5; ++w) sb->issued[w] = 0;
         sb->consumed = 0;
         sb->peer_abort = PAIR ? peer_addr(const_cast<const int*>(&sb->abort_flag), rank ^ 1u) : 0u;
         mbar_fence_init();
@@ -324,78 +324,66 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         w.nt = local / rows_g;
         return w;
     };
+    // bytes of B that producer `part` loads a stage: 64-column boxes in turn
+    auto b_share = [&](int part) {
+        if (!BMN) return p.b_bytes;
+        const int boxes = p.b_bytes / (BK * ROWB);
+        return (boxes + 1 - part) / 2 * (BK * ROWB);
+    };
     auto k_lo = [&](int split) { return (int)((int64_t)p.kb * split / p.splits); };
 
-    if (warp == 0) {
-        // ---------------- TMA producer
+    if (warp == 0 || warp == 2 || (AMN && warp == 3) || (BMN && warp == 4)) {
+        // ---------------- TMA producers, one load a stage each where it can
+        // be (a thread that issues two is slower than the MMAs: 0.46 us a
+        // stage, and 0.56 us with all four, against 0.36): warp 0 loads A and
+        // warp 2 B, warps 3 and 4 the second halves of MN-major ones
         if (lane == 0) {
-            // A may come from a kernel of this call that is still running, B
-            // (weights, x, the saved a) never does: the first stages' B loads go
-            // out before the wait.
+            const bool is_a = warp == 0 || warp == 3;
+            const int part = warp >= 3;
+            const bool remote = PAIR && !leader;
+            const uint32_t bytes = (uint32_t)(is_a ? (AMN ? p.a_bytes / 2 : p.a_bytes) : b_share(part));
+            int* issued = &sb->issued[warp];
+            // A may come from a kernel of this call that is still running; B
+            // (weights, x, the saved a) never does
+            if (is_a) grid_dep_wait();
             int it = 0, s = 0;
             uint32_t ph = 0;
-            int early = 0;      // stages whose barrier is armed and whose B load is out
-            const bool remote = PAIR && !leader;
-            auto bar_of = [&](int st) { return remote ? peer_addr(&sb->pfull[st], 0u) : smem_u32(&sb->full[st]); };
-            auto load = [&](const CUtensorMap* m, int st, uint32_t dst, int x, int y) {
-                if (remote) tma_load_2d_peer_bar(m, dst, bar_of(st), x, y);
-                else tma_load_2d(m, dst, &sb->full[st], x, y);
-            };
-            auto arm = [&](int st) {
-                if (remote) mbar_arrive_expect_tx_remote(bar_of(st), (uint32_t)stage_bytes);
-                else mbar_arrive_expect_tx(&sb->full[st], (uint32_t)stage_bytes);
-            };
-            auto load_b = [&](int st, int nt, int k0) {
-                const uint32_t b_dst = tiles_u32 + st * stage_bytes + p.a_bytes;
-                if constexpr (BMN) {
-                    const int n0 = nt * p.bn + (int)rank * (p.bn / 2);
-                    const int cols = PAIR ? p.bn / 2 : p.bn;
-                    for (int c = 0; c < cols; c += 64) load(&map_b, st, b_dst + c * ROWB, n0 + c, k0);
-                } else if constexpr (GLU) {
-                    // gate rows from nt * bn / 2, up rows N behind; a pair's second CTA stages the up rows
-                    const int n0 = nt * (p.bn / 2);
-                    load(&map_b, st, b_dst, k0, n0 + (PAIR ? (int)rank * p.N : 0));
-                    if (!PAIR) load(&map_b, st, b_dst + p.b_rows * ROWB, k0, n0 + p.N);
-                } else {
-                    load(&map_b, st, b_dst, k0, nt * p.bn + (int)rank * (p.bn / 2));
-                }
-            };
-            if (unit0 < num_units) {
-                const Where w = where(unit0);
-                const int klo = k_lo(w.split);
-                early = min(STAGES, k_lo(w.split + 1) - klo);
-                for (int e = 0; e < early; ++e) {
-                    arm(e);
-                    load_b(e, w.nt, (klo + e) * KSTEP);
-                    sb->issued = e + 1;
-                }
-            }
-            grid_dep_wait();
             for (int u = unit0; u < num_units && !sb->abort_flag; u += step) {
                 const Where w = where(u);
                 const int m0 = (w.row * NCTA + (int)rank) * BM;
                 const int kend = k_lo(w.split + 1);
                 bool ok = true;
                 for (int kb = k_lo(w.split); kb < kend; ++kb, ++it) {
+                    if (!wait_bounded(&sb->empty[s], ph ^ 1u, sb, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = remote ? peer_addr(&sb->full[s], 0u) : smem_u32(&sb->full[s]);
+                    auto load = [&](const CUtensorMap* m, uint32_t dst, int x, int y) {
+                        if (remote) tma_load_2d_peer_bar(m, dst, bar, x, y);
+                        else tma_load_2d(m, dst, &sb->full[s], x, y);
+                    };
+                    if (remote) mbar_arrive_expect_tx_remote(bar, bytes);
+                    else mbar_arrive_expect_tx(&sb->full[s], bytes);
                     const int k0 = kb * KSTEP;
-                    if (it >= early) {
-                        if (!wait_bounded<PAIR>(&sb->empty[s], ph ^ 1u, sb, p.status)) {
-                            ok = false;
-                            break;
-                        }
-                        arm(s);
-                    }
                     const uint32_t a_dst = tiles_u32 + s * stage_bytes;
-                    if constexpr (AMN) {
-                        load(&map_a, s, a_dst, m0, k0);
-                        load(&map_a, s, a_dst + BK * ROWB, m0 + 64, k0);
+                    const uint32_t b_dst = a_dst + p.a_bytes;
+                    if (is_a) {
+                        if (AMN) load(&map_a, a_dst + part * (BK * ROWB), m0 + part * 64, k0);
+                        else load(&map_a, a_dst, k0, m0);
+                    } else if constexpr (BMN) {
+                        const int n0 = w.nt * p.bn + (int)rank * (p.bn / 2);
+                        const int cols = PAIR ? p.bn / 2 : p.bn;
+                        for (int c = part * 64; c < cols; c += 128) load(&map_b, b_dst + c * ROWB, n0 + c, k0);
+                    } else if constexpr (GLU) {
+                        // gate rows from nt * bn / 2, up rows N behind; a pair's second CTA stages the up rows
+                        const int n0 = w.nt * (p.bn / 2);
+                        load(&map_b, b_dst, k0, n0 + (PAIR ? (int)rank * p.N : 0));
+                        if (!PAIR) load(&map_b, b_dst + p.b_rows * ROWB, k0, n0 + p.N);
                     } else {
-                        load(&map_a, s, a_dst, k0, m0);
+                        load(&map_b, b_dst, k0, w.nt * p.bn + (int)rank * (p.bn / 2));
                     }
-                    if (it >= early) {
-                        load_b(s, w.nt, k0);
-                        sb->issued = it + 1;
-                    }
+                    *issued = it + 1;
                     if (++s == STAGES) {
                         s = 0;
                         ph ^= 1u;
@@ -413,14 +401,13 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 const Where w = where(u);
                 const int acc = tc & 1;
                 const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
-                if (!wait_bounded<PAIR>(&sb->tempty[acc], aph ^ 1u, sb, p.status)) break;
+                if (!wait_bounded(&sb->tempty[acc], aph ^ 1u, sb, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * MAX_BN);
                 const int klo = k_lo(w.split), kend = k_lo(w.split + 1);
                 bool ok = true;
                 for (int kb = klo; kb < kend; ++kb, ++it) {
-                    if (!wait_bounded<PAIR>(&sb->full[s], ph, sb, p.status) ||
-                        (PAIR && !wait_bounded<PAIR>(&sb->pfull[s], ph, sb, p.status))) {
+                    if (!wait_bounded(&sb->full[s], ph, sb, p.status)) {
                         ok = false;
                         break;
                     }
@@ -447,9 +434,9 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 else umma_commit(&sb->tfull[acc]);
             }
         }
-    } else if (warp >= 4) {
-        // ---------------- epilogue
-        const int q = warp & 3, half = (warp - 4) >> 2;
+    } else if (warp >= EPI_WARP0) {
+        // ---------------- epilogue: a warp reads the TMEM lane quarter of its number
+        const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
         const uint32_t leader_tempty[2] = {PAIR ? peer_addr(&sb->tempty[0], 0u) : 0u, PAIR ? peer_addr(&sb->tempty[1], 0u) : 0u};
         int tc = 0;
         grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
@@ -475,7 +462,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 }
             };
             if constexpr (EPI == EPI_DGLU) fetch(half * 16);
-            const bool ok = wait_bounded<PAIR>(&sb->tfull[acc], aph, sb, p.status);
+            const bool ok = wait_bounded(&sb->tfull[acc], aph, sb, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
@@ -546,22 +533,19 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         aborted = aborted || ld_remote_s32(sb->peer_abort) != 0;
     }
     if (aborted) {
+        // copies issued but not consumed, the peer's among them; a stage that
+        // not every producer reached never completes, so one limit covers all
         if (warp == 0 && lane == 0 && (!PAIR || leader)) {
-            for (int it = sb->consumed; it < sb->issued; ++it) {
-                const long long t0 = clock64();
+            const long long t0 = clock64();
+            int to = 0;
+            for (int w = 0; w < 5; ++w) {
+                to = max(to, sb->issued[w]);
+                if (PAIR) to = max(to, ld_remote_s32(peer_addr(&sb->issued[w], 1u)));
+            }
+            for (int it = sb->consumed; it < to; ++it)
                 while (!mbar_try_wait(smem_u32(&sb->full[it % STAGES]), (uint32_t)(it / STAGES) & 1u) &&
                        clock64() - t0 < kWaitCycles) {
                 }
-            }
-            if (PAIR) {
-                const int peer_issued = ld_remote_s32(peer_addr(&sb->issued, 1u));
-                for (int it = sb->consumed; it < peer_issued; ++it) {
-                    const long long t0 = clock64();
-                    while (!mbar_try_wait(smem_u32(&sb->pfull[it % STAGES]), (uint32_t)(it / STAGES) & 1u) &&
-                           clock64() - t0 < kWaitCycles) {
-                    }
-                }
-            }
         }
         if (warp == 1 && lane == 0 && (!PAIR || leader)) {
             if constexpr (PAIR) umma_commit_pair_local(&sb->drain);
