@@ -352,7 +352,7 @@ class Engram:
         bf = torch.bfloat16
         n, f, a = self._ffn_args(x, Wgu, Wd, act, bf, bf)
         self._want("d_y", d_y, (n, self.cfg.hidden), bf)
-        self._want("saved", saved, (n * f * 2 + (n + 31) // 32 * 32 * f * 6,), torch.uint8)
+        self._want("saved", saved, (engram_ffn_saved_bytes(self.ctx, n, f),), torch.uint8)
         need = engram_ffn_grad_workspace_bytes(self.ctx, n, f)
         with _on_stream(stream):
             d_x, d_Wgu, d_Wd = torch.empty_like(x), torch.empty_like(Wgu), torch.empty_like(Wd)

@@ -46,6 +46,7 @@ constexpr int BK = 64;                  // contraction indices per stage of MN-m
 constexpr int A_BYTES = BM * ROWB;      // 16 KB
 constexpr int MAX_BN = 256;
 constexpr int EPI_WARPS = 8;
+constexpr int EPI_PARTS = EPI_WARPS / 4;   // warps per TMEM lane quarter, taking turns on 16-column chunks
 constexpr int EPI_WARP0 = 5;            // warps 0-4: producers and MMA issuer
 constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int TMEM_COLS = 512;
@@ -53,9 +54,12 @@ constexpr int TMEM_COLS = 512;
 // Shared memory: a ring of stages, each A rows then B rows of 128 bytes.  Few
 // rows stage only the rows they have, and a narrow tile only its columns, so
 // that more stages are in flight: the ring's round trip (free slot -> load ->
-// MMA -> free slot) is 1.4 us for one CTA and 2 us for a pair, and a stage
-// takes that over the number of stages at least.
-constexpr int TILE_AREA = 7 * 32768;    // seven stages of a 256 x 256 pair tile
+// MMA -> free slot) is about 1.4 us, and a stage takes that over the number of
+// stages at least.  A pair's epilogue keeps the last 64 KB for its patches,
+// which leaves five stages of a 256 x 256 tile (with three it is slower, with
+// seven no faster).
+constexpr int TILE_AREA = 7 * 32768;
+constexpr int STAGING = 65536;          // two 4 KB patches for each epilogue warp of a pair
 constexpr int MAX_STAGES = 14;
 constexpr int SMEM_BYTES = TILE_AREA + 1024 + 1024;   // ring | barriers | alignment
 
@@ -74,6 +78,7 @@ struct __align__(8) Barriers {
 
 struct FfnParams {
     int M, N;                   // output rows and columns (EPI_GLU: channels)
+    int64_t ldo;                // elements from one row of out to the next
     int kb;                     // stages along the contraction
     int bn;                     // accumulator columns per tile (EPI_GLU: gate and up together)
     int n_tiles, m_units, splits, raster;
@@ -209,41 +214,38 @@ struct Raw24 {
     }
 };
 
-// Eight columns from c of one row, wherever the sums came from.
-__device__ __forceinline__ void put_glu8(const FfnParams& p, int64_t row, int c, float* g, float* u) {
+// Eight columns from c of one row, wherever the sums came from; *_8 leave the
+// values to store in their arguments.
+__device__ __forceinline__ void glu8(const FfnParams& p, int64_t row, int c, float* g, const float* u) {
     if (p.gu_hi) {
         put24(p, at24(p, row, c), g);
         put24(p, at24(p, row, p.N + c), u);
     }
-    float a[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = g[k] * act_p(g[k], p.act) * u[k];
-    store8(p.out + row * p.N + c, a);
+    for (int k = 0; k < 8; ++k) g[k] *= act_p(g[k], p.act) * u[k];
 }
 
-__device__ __forceinline__ void put_dglu8(const FfnParams& p, int64_t row, int c, const float* da, const Raw24& rg,
-                                          const Raw24& ru) {
-    float g[8], u[8], dg[8], du[8];
+__device__ __forceinline__ void dglu8(const FfnParams& p, const Raw24& rg, const Raw24& ru, float* dg, float* du) {
+    float g[8], u[8];
     rg.get(g);
     ru.get(u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float pr = act_p(g[k], p.act);
-        du[k] = da[k] * (g[k] * pr);
-        dg[k] = da[k] * u[k] * act_d(g[k], pr, p.act);
+        const float da = dg[k], pr = act_p(g[k], p.act);
+        du[k] = da * (g[k] * pr);
+        dg[k] = da * u[k] * act_d(g[k], pr, p.act);
     }
-    store8(p.out + row * 2 * p.N + c, dg);
-    store8(p.out + row * 2 * p.N + p.N + c, du);
 }
 
-__device__ __forceinline__ void put_out8(const FfnParams& p, int64_t row, int c, float* v) {
-    if (p.res) {
-        float r[8];
-        load8(p.res + row * p.N + c, r);
+__device__ __forceinline__ void add8(float* v, const uint4& r) {
+    float f[8];
+    load8(reinterpret_cast<const __nv_bfloat16*>(&r), f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += r[k];
-    }
-    store8(p.out + row * p.N + c, v);
+    for (int k = 0; k < 8; ++k) v[k] += f[k];
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
 // ---------------------------------------------------------------- kernel
@@ -436,14 +438,43 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         }
     } else if (warp >= EPI_WARP0) {
         // ---------------- epilogue: a warp reads the TMEM lane quarter of its number
-        const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
+        const int q = warp & 3, part = (warp - EPI_WARP0) >> 2;
         const uint32_t leader_tempty[2] = {PAIR ? peer_addr(&sb->tempty[0], 0u) : 0u, PAIR ? peer_addr(&sb->tempty[1], 0u) : 0u};
+        // A warp takes blocks of BLK columns in turn with the others of its
+        // lane quarter.  STAGED: its lanes, a row each, leave their bf16 values
+        // in a patch of shared memory [32 rows][128 bytes] (16-byte chunks
+        // swizzled by the row), and the patch goes out four full lines per
+        // instruction; by rows, a store touches 32 lines of 16 bytes.
+        constexpr bool STAGED = PAIR && EPI != EPI_PART;
+        constexpr int BLK = STAGED ? 64 : 16;
+        uint8_t* patch = smem + TILE_AREA - STAGING + (warp - EPI_WARP0) * (STAGING / EPI_WARPS);
+        auto patch_at = [&](int k, int r, int ch) {
+            return reinterpret_cast<uint4*>(patch + k * 4096 + r * 128 + ((ch ^ (r & 7)) << 4));
+        };
+        auto next_chunk = [&](int c) { return (c + 16) % BLK ? c + 16 : c + 16 + BLK * (EPI_PARTS - 1); };
         int tc = 0;
         grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
+        // DGLU: this warp's g and u of a tile into L2, a tile ahead
+        auto prefetch_gu = [&](int u) {
+            const Where w = where(u);
+            const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
+            if (row >= p.M) return;
+            for (int c = part * BLK; c < p.bn; c = next_chunk(c)) {
+                const int col = w.nt * p.bn + c;
+                if (col >= p.N) break;
+                // 16 columns: two elements of the high plane (512 bytes each) and two of the low one, of g and u
+                const int64_t at = at24(p, row, (lane & 1) ? p.N + col : col);
+                const int line = lane >> 1;
+                if (line < 8) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.gu_hi + at) + line * 128));
+                else if (line < 12) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.gu_lo + at) + (line - 8) * 128));
+            }
+        };
+        if (EPI == EPI_DGLU && unit0 < num_units) prefetch_gu(unit0);
         for (int u = unit0; u < num_units; u += step, ++tc) {
             const Where w = where(u);
             const int acc = tc & 1;
             const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
+            if (EPI == EPI_DGLU && u + step < num_units) prefetch_gu(u + step);
             const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
             const bool live = row < p.M;
             const int width = GLU ? p.bn / 2 : p.bn;       // output columns of the tile
@@ -461,61 +492,101 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     }
                 }
             };
-            if constexpr (EPI == EPI_DGLU) fetch(half * 16);
+            if constexpr (EPI == EPI_DGLU) fetch(part * BLK);
             const bool ok = wait_bounded(&sb->tfull[acc], aph, sb, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
             float rs = 1.f;
             if (F8 && live) rs = __ldg(p.row_scale + row);
+            // the patch's lane: row r of four, 16-byte chunk lane % 8
+            auto each_line = [&](int b0, auto&& f) {
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r = it * 4 + (lane >> 3), ch = lane & 7;
+                    const int64_t to_row = row - lane + r;
+                    const int col = c_tile + b0 + ch * 8;
+                    if (to_row < p.M && b0 + ch * 8 < width && col < p.N) f(r, ch, to_row, col);
+                }
+            };
 #pragma unroll 1
-            for (int c = half * 16; c < width; c += 32) {
-                uint32_t x[16], y[16];
-                tmem_ld16(taddr + c, x);
-                if (GLU) tmem_ld16(taddr + width + c, y);
-                Raw24 cg[2], cu[2];
-                if constexpr (EPI == EPI_DGLU) {
+            for (int b0 = part * BLK; b0 < width; b0 += BLK * EPI_PARTS) {
+                if (STAGED && EPI == EPI_OUT && p.res) {
+                    each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
+                        *patch_at(0, r, ch) = *reinterpret_cast<const uint4*>(p.res + to_row * p.N + col);
+                    });
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (int c = b0; c < min(b0 + BLK, width); c += 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld16(taddr + c, x);
+                    if (GLU) tmem_ld16(taddr + width + c, y);
+                    Raw24 cg[2], cu[2];
+                    if constexpr (EPI == EPI_DGLU) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            cg[h] = rg[h];
+                            cu[h] = ru[h];
+                        }
+                        if (next_chunk(c) < width) fetch(next_chunk(c));
+                    }
+                    tmem_wait_ld(x);
+                    if (GLU) tmem_wait_ld(y);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        cg[h] = rg[h];
-                        cu[h] = ru[h];
-                    }
-                    if (c + 32 < width) fetch(c + 32);
-                }
-                tmem_wait_ld(x);
-                if (GLU) tmem_wait_ld(y);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = c_tile + c + h * 8;
-                    if (!live || c + h * 8 >= width || col >= p.N) continue;
-                    float f[8], g[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        f[k] = __uint_as_float(x[h * 8 + k]);
-                        if (GLU) g[k] = __uint_as_float(y[h * 8 + k]);
-                    }
-                    if constexpr (F8) {
+                        const int col = c_tile + c + h * 8;
+                        if (!live || c + h * 8 >= width || col >= p.N) continue;
+                        float f[8], g[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            f[k] *= rs * __ldg(p.col_scale + col + k);
-                            g[k] *= rs * __ldg(p.col_scale + p.N + col + k);
+                            f[k] = __uint_as_float(x[h * 8 + k]);
+                            if (GLU) g[k] = __uint_as_float(y[h * 8 + k]);
+                        }
+                        if constexpr (F8) {
+                            float sf[8], sg[8];
+                            Vec<float>::load(p.col_scale + col, sf);
+                            Vec<float>::load(p.col_scale + col + 4, sf + 4);
+                            Vec<float>::load(p.col_scale + p.N + col, sg);
+                            Vec<float>::load(p.col_scale + p.N + col + 4, sg + 4);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                f[k] *= rs * sf[k];
+                                g[k] *= rs * sg[k];
+                            }
+                        }
+                        const int ch = (c - b0) / 8 + h;
+                        if constexpr (EPI == EPI_PART) {
+                            const int64_t ld = GLU ? 2 * (int64_t)p.N : p.N;
+                            float* to = p.part + ((int64_t)w.split * p.M + row) * ld + col;
+                            Vec<float>::store(to, f);
+                            Vec<float>::store(to + 4, f + 4);
+                            if (GLU) {
+                                Vec<float>::store(to + p.N, g);
+                                Vec<float>::store(to + p.N + 4, g + 4);
+                            }
+                        } else {
+                            if constexpr (EPI == EPI_GLU) glu8(p, row, col, f, g);
+                            if constexpr (EPI == EPI_DGLU) dglu8(p, cg[h], cu[h], f, g);
+                            if constexpr (EPI == EPI_OUT) {
+                                if (p.res)
+                                    add8(f, STAGED ? *patch_at(0, lane, ch) : *reinterpret_cast<const uint4*>(p.res + row * p.N + col));
+                            }
+                            *(STAGED ? patch_at(0, lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + col)) = pack8(f);
+                            if constexpr (EPI == EPI_DGLU)
+                                *(STAGED ? patch_at(1, lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + col)) = pack8(g);
                         }
                     }
-                    if constexpr (EPI == EPI_GLU) put_glu8(p, row, col, f, g);
-                    if constexpr (EPI == EPI_DGLU) put_dglu8(p, row, col, f, cg[h], cu[h]);
-                    if constexpr (EPI == EPI_OUT) put_out8(p, row, col, f);
-                    if constexpr (EPI == EPI_PART) {
-                        const int64_t ld = GLU ? 2 * (int64_t)p.N : p.N;
-                        float* to = p.part + ((int64_t)w.split * p.M + row) * ld + col;
-                        Vec<float>::store(to, f);
-                        Vec<float>::store(to + 4, f + 4);
-                        if (GLU) {
-                            Vec<float>::store(to + p.N, g);
-                            Vec<float>::store(to + p.N + 4, g + 4);
-                        }
-                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if constexpr (STAGED) {
+                    each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
+                        __nv_bfloat16* to = p.out + to_row * p.ldo + col;
+                        *reinterpret_cast<uint4*>(to) = *patch_at(0, r, ch);
+                        if (EPI == EPI_DGLU) *reinterpret_cast<uint4*>(to + p.N) = *patch_at(1, r, ch);
+                    });
+                    __syncwarp();
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -589,23 +660,40 @@ __global__ void ffn_join_kernel(const FfnParams p) {
             add(f, from);
             if (EPI == EPI_GLU) add(g, from + p.N);
         }
-        if constexpr (EPI == EPI_GLU) put_glu8(p, row, c, f, g);
+        if constexpr (EPI == EPI_GLU) glu8(p, row, c, f, g);
         if constexpr (EPI == EPI_DGLU) {
             Raw24 rg, ru;
             rg.load(p, at24(p, row, c));
             ru.load(p, at24(p, row, p.N + c));
-            put_dglu8(p, row, c, f, rg, ru);
+            dglu8(p, rg, ru, f, g);
+            *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
         }
-        if constexpr (EPI == EPI_OUT) put_out8(p, row, c, f);
+        if constexpr (EPI == EPI_OUT) {
+            if (p.res) add8(f, *reinterpret_cast<const uint4*>(p.res + row * p.N + c));
+        }
+        *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
     }
 }
 
 // ---------------------------------------------------------------- host side
 
 // [rows][cols] row-major operand; boxes of 128 bytes of a row x box_rows rows
-bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows, bool f8) {
-    return make_map(m, base, (uint64_t)rows, (uint64_t)cols, (uint32_t)box_rows, f8);
+// ld elements apart; rows and columns outside read as zero
+bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f8) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t es = f8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)(ROWB / es), (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Row pitch of the matrices this file keeps between products (a, [dg du]):
+// whole 128-byte lines, or a row of a tile would touch five sectors for four
+// (down projection of 16372 rows, f 6824: DOWN_FIG).
+int64_t pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 // How a product is cut: one CTA or a pair per tile, accumulator columns,
 // splits of the contraction, bytes and number of the stages.
@@ -636,8 +724,8 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
         const int64_t tiles = m_units * n_tiles;
         const int a_bytes = a_rows * ROWB, b_bytes = (pair ? bn / 2 : bn) * ROWB;
         // the MMA reads 128 rows of A whatever was staged: the last stage's lie inside the ring too
-        const int stages = std::min(MAX_STAGES, (TILE_AREA - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
-        const double stage = std::max(std::max(0.365 * bn / 256, (pair ? 2.0 : 1.4) / stages), (a_bytes + b_bytes) / 80e3);
+        const int stages = std::min(MAX_STAGES, (TILE_AREA - (pair ? STAGING : 0) - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
+        const double stage = std::max(std::max(0.365 * bn / 256, 1.4 / stages), (a_bytes + b_bytes) / 80e3);
         for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
             if (splits > 1 && tiles * (splits - 1) >= workers) break;
             const int64_t waves = (tiles * splits + workers - 1) / workers;
@@ -710,8 +798,8 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
 // One product: A [M][K] (or [K][M] with AMN), B [N][K] (or [K][N] with BMN;
 // GLU: [2N][K]), and its epilogue, through partial sums when the plan splits.
 template <int EPI, bool AMN, bool BMN, bool F8 = false>
-cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int64_t N, int64_t K, FfnParams p, float* part,
-                    const char* name, bool after, cudaStream_t s) {
+cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                    FfnParams p, float* part, const char* name, bool after, cudaStream_t s) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int kstep = F8 ? 128 : 64;
     const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, AMN, BMN);
@@ -735,8 +823,8 @@ cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int6
               ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((pl.pair ? 256 : 128) >> 4) << 24);
     CUtensorMap ma, mb;
     const int64_t b_cols = GLU ? 2 * N : N;
-    const bool ok = (AMN ? operand_map(&ma, A, K, M, BK, F8) : operand_map(&ma, A, M, K, pl.a_bytes / ROWB, F8)) &&
-                    (BMN ? operand_map(&mb, B, K, b_cols, BK, F8) : operand_map(&mb, B, b_cols, K, p.b_rows, F8));
+    const bool ok = (AMN ? operand_map(&ma, A, K, M, lda, BK, F8) : operand_map(&ma, A, M, K, lda, pl.a_bytes / ROWB, F8)) &&
+                    (BMN ? operand_map(&mb, B, K, b_cols, ldb, BK, F8) : operand_map(&mb, B, b_cols, K, ldb, p.b_rows, F8));
     if (!ok) return cudaErrorInvalidValue;
     prof_begin(c, s, name);
     cudaError_t e;
@@ -769,7 +857,7 @@ cudaError_t product(engram_ctx* c, const void* A, const void* B, int64_t M, int6
 // What the forward keeps for the backward: the two planes of g and u, and
 // a = act(g) u as the down projection read it.
 struct Saved {
-    __nv_bfloat16* a;       // [n][f]
+    __nv_bfloat16* a;       // [n][f], rows pitch(f) apart
     uint4* hi;              // [ceil(n / 32)][2f / 8][32]
     uint2* lo;
     size_t bytes;
@@ -778,8 +866,9 @@ struct Saved {
 Saved saved_of(const void* base, int64_t n, int64_t f) {
     char* p = static_cast<char*>(const_cast<void*>(base));
     const int64_t elems = (n + 31) / 32 * 32 * (f / 4);
-    return Saved{reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<uint4*>(p + n * f * 2),
-                 reinterpret_cast<uint2*>(p + n * f * 2 + elems * 16), (size_t)(n * f * 2 + elems * 24)};
+    const int64_t a_bytes = n * pitch(f) * 2;
+    return Saved{reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<uint4*>(p + a_bytes),
+                 reinterpret_cast<uint2*>(p + a_bytes + elems * 16), (size_t)(a_bytes + elems * 24)};
 }
 
 // Scratch: the products' shared partial sums, then the intermediate matrix
@@ -812,7 +901,7 @@ FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad
         return q;
     };
     w.part = reinterpret_cast<float*>(take(part));
-    w.mid = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * f * (grad ? 4 : 2)));
+    w.mid = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * pitch(grad ? 2 * f : f) * 2));
     w.bytes = (size_t)(p - static_cast<char*>(base));
     return w;
 }
@@ -868,8 +957,9 @@ engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int
     if (!x || !Wgu || !Wd || !y) return inval("null tensor pointer");
     if (f8 ? (!x_scale || !gu_scale) : (x_scale || gu_scale))
         return inval("x_scale and gu_scale go with ENGRAM_FP8, and are required there");
-    if (!aligned16(x) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(res) || !aligned16(y) || !aligned16(saved))
-        return inval("x, Wgu, Wd, res, y and saved must be 16-byte aligned");
+    if (!aligned16(x) || !aligned16(Wgu) || !aligned16(Wd) || !aligned16(res) || !aligned16(y) || !aligned16(saved) ||
+        !aligned16(gu_scale))
+        return inval("x, Wgu, gu_scale, Wd, res, y and saved must be 16-byte aligned");
     const FfnWs w = ffn_carve(c, workspace, n, f, false);
     st = check_ws(workspace, workspace_bytes, w.bytes);
     if (st == ENGRAM_OK) st = check_device(c);
@@ -879,6 +969,7 @@ engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int
     FfnParams p{};
     p.act = act;
     p.out = w.mid;
+    p.ldo = pitch(f);
     if (saved) {
         const Saved sv = saved_of(saved, n, f);
         p.out = sv.a;
@@ -887,13 +978,14 @@ engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int
     }
     p.row_scale = x_scale;
     p.col_scale = gu_scale;
-    cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up_fp8", false, s)
-                       : product<EPI_GLU, false, false>(c, x, Wgu, n, f, d, p, w.part, "ffn_gate_up", false, s);
+    cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, d, Wgu, d, n, f, d, p, w.part, "ffn_gate_up_fp8", false, s)
+                       : product<EPI_GLU, false, false>(c, x, d, Wgu, d, n, f, d, p, w.part, "ffn_gate_up", false, s);
     if (e != cudaSuccess) return cuda_fail("feed-forward gate/up launch", e);
     FfnParams o{};
     o.out = static_cast<__nv_bfloat16*>(y);
+    o.ldo = d;
     o.res = static_cast<const __nv_bfloat16*>(res);
-    e = product<EPI_OUT, false, false>(c, p.out, Wd, n, d, f, o, w.part, "ffn_down", true, s);
+    e = product<EPI_OUT, false, false>(c, p.out, p.ldo, Wd, f, n, d, f, o, w.part, "ffn_down", true, s);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward down launch", e);
 }
 
@@ -936,21 +1028,24 @@ engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, con
     p.act = act;
     const Saved sv = saved_of(saved, n, f);
     p.out = w.mid;
+    p.ldo = pitch(2 * (int64_t)f);
     p.gu_hi = sv.hi;
     p.gu_lo = sv.lo;
-    cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, Wd, n, f, d, p, w.part, "ffn_d_gate_up", false, s);
+    cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, d, Wd, f, n, f, d, p, w.part, "ffn_d_gate_up", false, s);
     FfnParams o{};
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_x);
-        e = product<EPI_OUT, false, true>(c, w.mid, Wgu, n, d, 2 * (int64_t)f, o, w.part, "ffn_d_x", true, s);
+        o.ldo = d;
+        e = product<EPI_OUT, false, true>(c, w.mid, p.ldo, Wgu, d, n, d, 2 * (int64_t)f, o, w.part, "ffn_d_x", true, s);
     }
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_Wgu);
-        e = product<EPI_OUT, true, true>(c, w.mid, x, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", true, s);
+        e = product<EPI_OUT, true, true>(c, w.mid, p.ldo, x, d, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", true, s);
     }
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_Wd);
-        e = product<EPI_OUT, true, true>(c, d_y, sv.a, d, f, n, o, w.part, "ffn_d_Wd", true, s);
+        o.ldo = f;
+        e = product<EPI_OUT, true, true>(c, d_y, d, sv.a, pitch(f), d, f, n, o, w.part, "ffn_d_Wd", true, s);
     }
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward backward launches", e);
 }

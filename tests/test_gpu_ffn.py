@@ -40,15 +40,16 @@ def inputs(n, d, f, seed=1):
 
 
 def planes(saved, n, f):
-    """(g and u [n][2f] fp32, a [n][f] bf16) of what the forward saves: a, then two planes of 8-column elements
-    blocked [row / 32][column / 8][row % 32]"""
-    rb, cut = (n + 31) // 32, n * f * 2
+    """(g and u [n][2f] fp32, a [n][f] bf16) of what the forward saves: a (rows of whole 128-byte lines), then two
+    planes of 8-column elements blocked [row / 32][column / 8][row % 32]"""
+    rb, ld = (n + 31) // 32, (f + 63) // 64 * 64
+    cut = n * ld * 2
     elems = rb * 32 * (f // 4)
     shape = (rb, f // 4, 32, 8)
     hi = saved[cut:cut + elems * 16].view(torch.int16).view(shape).to(torch.int32) << 16
     lo = saved[cut + elems * 16:].view(shape).to(torch.int32) << 8
     gu = (hi | lo).permute(0, 2, 1, 3).reshape(rb * 32, 2 * f)[:n].contiguous().view(torch.float32)
-    return gu, saved[:cut].view(torch.bfloat16).view(n, f)
+    return gu, saved[:cut].view(torch.bfloat16).view(n, ld)[:, :f]
 
 
 def check_forward(y, saved, x, Wgu, Wd, kind, res=None):
