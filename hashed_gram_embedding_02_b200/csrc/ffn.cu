@@ -165,7 +165,6 @@ __device__ __forceinline__ float act_d(float g, float p, int act) {
 }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) { Vec<__nv_bfloat16>::load(p, f); }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) { Vec<__nv_bfloat16>::store(p, f); }
 
 // g and u are kept for the backward as 24 of their 32 bits (half a step 2^-16):
 // in bf16 their rounding would reach d_x and d_Wgu beside that of dg and du
@@ -174,6 +173,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) { Vec<_
 // epilogues hold them, [row / 32][column / 8][row % 32] elements of 8 columns:
 // a warp's access is contiguous, where rows of 2 N would touch 32 lines
 // (d_gate_up of 16372 rows, d 2560, f 6824: 1343 us by rows, 673 us blocked).
+// Prefetching a tile of them into L2 ahead costs 45 us more than it saves.
 __device__ __forceinline__ int64_t at24(const FfnParams& p, int64_t row, int col) {
     return ((row >> 5) * (p.N / 4) + col / 8) * 32 + (row & 31);
 }
@@ -200,8 +200,8 @@ struct Raw24 {
     uint4 hi;
     uint2 lo;
     __device__ __forceinline__ void load(const FfnParams& p, int64_t at) {
-        hi = __ldg(p.gu_hi + at);
-        lo = __ldg(p.gu_lo + at);
+        hi = __ldcs(p.gu_hi + at);     // read once: leaves L2 to the operands
+        lo = __ldcs(p.gu_lo + at);
     }
     __device__ __forceinline__ void get(float* f) const {
         const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
@@ -451,48 +451,34 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         auto patch_at = [&](int k, int r, int ch) {
             return reinterpret_cast<uint4*>(patch + k * 4096 + r * 128 + ((ch ^ (r & 7)) << 4));
         };
-        auto next_chunk = [&](int c) { return (c + 16) % BLK ? c + 16 : c + 16 + BLK * (EPI_PARTS - 1); };
+        // the warp's k-th chunk of 16 columns
+        auto chunk = [&](int k) { return part * BLK + k / (BLK / 16) * (BLK * EPI_PARTS) + k % (BLK / 16) * 16; };
         int tc = 0;
         grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
-        // DGLU: this warp's g and u of a tile into L2, a tile ahead
-        auto prefetch_gu = [&](int u) {
-            const Where w = where(u);
-            const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
-            if (row >= p.M) return;
-            for (int c = part * BLK; c < p.bn; c = next_chunk(c)) {
-                const int col = w.nt * p.bn + c;
-                if (col >= p.N) break;
-                // 16 columns: two elements of the high plane (512 bytes each) and two of the low one, of g and u
-                const int64_t at = at24(p, row, (lane & 1) ? p.N + col : col);
-                const int line = lane >> 1;
-                if (line < 8) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.gu_hi + at) + line * 128));
-                else if (line < 12) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.gu_lo + at) + (line - 8) * 128));
-            }
-        };
-        if (EPI == EPI_DGLU && unit0 < num_units) prefetch_gu(unit0);
         for (int u = unit0; u < num_units; u += step, ++tc) {
             const Where w = where(u);
             const int acc = tc & 1;
             const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
-            if (EPI == EPI_DGLU && u + step < num_units) prefetch_gu(u + step);
             const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
             const bool live = row < p.M;
             const int width = GLU ? p.bn / 2 : p.bn;       // output columns of the tile
             const int c_tile = w.nt * width;
-            // g and u of the next 16 columns are loaded while the current ones are worked on, the tile's
-            // first ones while its MMAs run
-            Raw24 rg[2], ru[2];
-            auto fetch = [&](int c) {
+            // g and u of two chunks are held or in flight, the tile's first ones while its MMAs run
+            Raw24 rg[2][2], ru[2][2];
+            auto fetch = [&](int c, Raw24* fg, Raw24* fu) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int col = c_tile + c + h * 8;
                     if (live && c + h * 8 < width && col < p.N) {
-                        rg[h].load(p, at24(p, row, col));
-                        ru[h].load(p, at24(p, row, p.N + col));
+                        fg[h].load(p, at24(p, row, col));
+                        fu[h].load(p, at24(p, row, p.N + col));
                     }
                 }
             };
-            if constexpr (EPI == EPI_DGLU) fetch(part * BLK);
+            if constexpr (EPI == EPI_DGLU) {
+                fetch(chunk(0), rg[0], ru[0]);
+                fetch(chunk(1), rg[1], ru[1]);
+            }
             const bool ok = wait_bounded(&sb->tfull[acc], aph, sb, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -509,28 +495,22 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (to_row < p.M && b0 + ch * 8 < width && col < p.N) f(r, ch, to_row, col);
                 }
             };
+            const int nk = STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4 : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
 #pragma unroll 1
-            for (int b0 = part * BLK; b0 < width; b0 += BLK * EPI_PARTS) {
-                if (STAGED && EPI == EPI_OUT && p.res) {
-                    each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
-                        *patch_at(0, r, ch) = *reinterpret_cast<const uint4*>(p.res + to_row * p.N + col);
-                    });
-                    __syncwarp();
-                }
-#pragma unroll 1
-                for (int c = b0; c < min(b0 + BLK, width); c += 16) {
+            for (int k2 = 0; k2 < nk; k2 += 2) {
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    const int k = k2 + odd, c = chunk(k), b0 = c / BLK * BLK;
+                    if (b0 >= width) break;
+                    if (STAGED && EPI == EPI_OUT && p.res && k % 4 == 0) {
+                        each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
+                            *patch_at(0, r, ch) = *reinterpret_cast<const uint4*>(p.res + to_row * p.N + col);
+                        });
+                        __syncwarp();
+                    }
                     uint32_t x[16], y[16];
                     tmem_ld16(taddr + c, x);
                     if (GLU) tmem_ld16(taddr + width + c, y);
-                    Raw24 cg[2], cu[2];
-                    if constexpr (EPI == EPI_DGLU) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            cg[h] = rg[h];
-                            cu[h] = ru[h];
-                        }
-                        if (next_chunk(c) < width) fetch(next_chunk(c));
-                    }
                     tmem_wait_ld(x);
                     if (GLU) tmem_wait_ld(y);
 #pragma unroll
@@ -567,7 +547,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                             }
                         } else {
                             if constexpr (EPI == EPI_GLU) glu8(p, row, col, f, g);
-                            if constexpr (EPI == EPI_DGLU) dglu8(p, cg[h], cu[h], f, g);
+                            if constexpr (EPI == EPI_DGLU) dglu8(p, rg[odd][h], ru[odd][h], f, g);
                             if constexpr (EPI == EPI_OUT) {
                                 if (p.res)
                                     add8(f, STAGED ? *patch_at(0, lane, ch) : *reinterpret_cast<const uint4*>(p.res + row * p.N + col));
@@ -577,15 +557,16 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                                 *(STAGED ? patch_at(1, lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + col)) = pack8(g);
                         }
                     }
+                    if constexpr (EPI == EPI_DGLU) fetch(chunk(k + 2), rg[odd], ru[odd]);
                     __syncwarp();
-                }
-                if constexpr (STAGED) {
-                    each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
-                        __nv_bfloat16* to = p.out + to_row * p.ldo + col;
-                        *reinterpret_cast<uint4*>(to) = *patch_at(0, r, ch);
-                        if (EPI == EPI_DGLU) *reinterpret_cast<uint4*>(to + p.N) = *patch_at(1, r, ch);
-                    });
-                    __syncwarp();
+                    if (STAGED && k % 4 == 3) {
+                        each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
+                            __nv_bfloat16* to = p.out + to_row * p.ldo + col;
+                            *reinterpret_cast<uint4*>(to) = *patch_at(0, r, ch);
+                            if (EPI == EPI_DGLU) *reinterpret_cast<uint4*>(to + p.N) = *patch_at(1, r, ch);
+                        });
+                        __syncwarp();
+                    }
                 }
             }
             tc_fence_before();
@@ -692,7 +673,7 @@ bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
 
 // Row pitch of the matrices this file keeps between products (a, [dg du]):
 // whole 128-byte lines, or a row of a tile would touch five sectors for four
-// (down projection of 16372 rows, f 6824: DOWN_FIG).
+// (down projection of 16372 rows, f 6824: 478 us, on lines 400 us).
 int64_t pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 
 // How a product is cut: one CTA or a pair per tile, accumulator columns,
