@@ -32,15 +32,26 @@ from .binding import (  # noqa: F401  (re-exported C ABI names)
     engram_workspace_bytes, make_config)
 
 
+class _Here:
+    """No change of stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+_HERE = _Here()
+
+
 def _on_stream(stream):
     """Context in which tensors are allocated for work on `stream` (a torch
     stream, a raw handle, or None: the current stream), so that the caching
     allocator hands their memory on only in that stream's order."""
-    import contextlib
-
-    import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
+    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -204,25 +215,23 @@ class Engram:
 
     def _want(self, name: str, t, shape, dtype):
         """Refuse a tensor of another device, dtype or shape, or with gaps."""
+        if t.shape == shape and t.dtype is dtype and t.device == self.device and t.is_contiguous():
+            return
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the context on {self.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} is {t.dtype}, needs {dtype}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t
+        raise ValueError(f"{name} must be contiguous")
 
     def _want_tokens(self, tok, t_begin: int):
         """(B, T, row stride) of a token tensor whose rows may be wider than T."""
         import torch
         if tok.dim() != 2:
             raise ValueError(f"tok has {tok.dim()} dimensions, needs 2")
-        if tok.device != self.device:
-            raise ValueError(f"tok is on {tok.device}, the context on {self.device}")
-        if tok.dtype != torch.int32:
-            raise ValueError(f"tok is {tok.dtype}, needs torch.int32")
+        if tok.dtype is not torch.int32 or tok.device != self.device:
+            raise ValueError(f"tok is {tok.dtype} on {tok.device}, needs torch.int32 on {self.device}")
         B, T = tok.shape
         if T > 1 and tok.stride(1) != 1:
             raise ValueError("the ids of a sequence must be adjacent in memory")

@@ -21,6 +21,8 @@
 //      the same for every piece however often a token occurs, so a token that
 //      takes half of the batch costs nothing extra.
 //   3. join: the parts of each cut run, in order.
+// Meanwhile the rows of the tokens that do not occur are cleared on the
+// context's side stream.
 // The order of every sum depends on the tokens alone.
 #include <algorithm>
 
@@ -67,36 +69,55 @@ struct TokSource {
 
 // ---------------------------------------------------------------- forward
 
-// One CTA takes `rb` groups of RPT rows; a thread holds one 16-byte chunk of
-// each of its RPT rows in flight.
+// Persistent: a CTA takes blockDim.y * RPT rows at a time, with the rows of the
+// next group and the tokens of the one after it in flight.
+constexpr int kEmbedRows = 2;
+
 template <typename T, int RPT>
 __global__ void embed_kernel(TokSource src, int64_t n, const T* __restrict__ E, float scale, T* __restrict__ h,
                              int cpr, uint32_t* status) {
     constexpr int EPC = Vec<T>::N;
-    const int64_t row0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * RPT;
-    const T* from[RPT];
-#pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-        from[r] = nullptr;
-        if (row0 + r < n) {
-            const int32_t v = src.at(row0 + r);
-            if (v >= 0 && v < src.V) from[r] = E + (int64_t)v * cpr * EPC;
-            else if (threadIdx.x == 0) flag(status, ENGRAM_ERR_TOKEN);
-        }
-    }
+    const int64_t first = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * RPT;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y * RPT;
     for (int c = threadIdx.x; c < cpr; c += blockDim.x) {
+        int32_t tok[RPT];
         uint4 q[RPT];
+        auto tokens = [&](int64_t r0) {
 #pragma unroll
-        for (int r = 0; r < RPT; ++r)
-            q[r] = from[r] ? __ldg(reinterpret_cast<const uint4*>(from[r]) + c) : make_uint4(0, 0, 0, 0);
+            for (int r = 0; r < RPT; ++r) tok[r] = r0 + r < n ? src.at(r0 + r) : 0;
+        };
+        auto rows = [&](uint4* to) {
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-            if (row0 + r >= n) break;
-            float f[EPC];
-            Vec<T>::load(reinterpret_cast<const T*>(&q[r]), f);
+            for (int r = 0; r < RPT; ++r)
+                to[r] = tok[r] >= 0 && tok[r] < src.V ? __ldg(reinterpret_cast<const uint4*>(E) + (int64_t)tok[r] * cpr + c)
+                                                      : make_uint4(0, 0, 0, 0);
+        };
+        auto check = [&]() {
+            if (c != 0) return;
 #pragma unroll
-            for (int k = 0; k < EPC; ++k) f[k] *= scale;
-            Vec<T>::store(h + ((row0 + r) * cpr + c) * EPC, f);
+            for (int r = 0; r < RPT; ++r)
+                if (tok[r] < 0 || tok[r] >= src.V) flag(status, ENGRAM_ERR_TOKEN);
+        };
+        tokens(first);
+        check();
+        rows(q);
+        tokens(first + step);
+        for (int64_t r0 = first; r0 < n; r0 += step) {
+            uint4 next[RPT];
+            check();
+            rows(next);
+            tokens(r0 + 2 * step);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                if (r0 + r < n) {
+                    float f[EPC];
+                    Vec<T>::load(reinterpret_cast<const T*>(&q[r]), f);
+#pragma unroll
+                    for (int k = 0; k < EPC; ++k) f[k] *= scale;
+                    Vec<T>::store(h + ((r0 + r) * cpr + c) * EPC, f);
+                }
+                q[r] = next[r];
+            }
         }
     }
 }
@@ -107,15 +128,15 @@ cudaError_t launch_embed(const TokSource& src, int64_t n, const void* E, float s
     const int cpr = d / Vec<T>::N;
     const RowGeo g = row_geo(cpr);
     const dim3 block(g.tpr, g.rb);
-    if (n >= (int64_t)num_sms * 16 * g.rb) {
-        constexpr int RPT = 4;
-        const int64_t per = (int64_t)g.rb * RPT;
-        embed_kernel<T, RPT><<<(unsigned)((n + per - 1) / per), block, 0, s>>>(
+    const int per_sm = std::max(1, 1280 / (g.tpr * g.rb));
+    auto go = [&](auto kern, int rpt) {
+        const int64_t groups = (n + (int64_t)g.rb * rpt - 1) / ((int64_t)g.rb * rpt);
+        kern<<<(unsigned)std::min<int64_t>(groups, (int64_t)num_sms * per_sm), block, 0, s>>>(
             src, n, static_cast<const T*>(E), scale, static_cast<T*>(h), cpr, status);
-    } else {
-        embed_kernel<T, 1><<<(unsigned)((n + g.rb - 1) / g.rb), block, 0, s>>>(
-            src, n, static_cast<const T*>(E), scale, static_cast<T*>(h), cpr, status);
-    }
+    };
+    // a short call spreads its rows over the SMs one by one
+    if (n >= (int64_t)num_sms * per_sm * g.rb * kEmbedRows) go(embed_kernel<T, kEmbedRows>, kEmbedRows);
+    else go(embed_kernel<T, 1>, 1);
     return cudaGetLastError();
 }
 
@@ -154,17 +175,13 @@ __device__ __forceinline__ uint32_t warp_rank(uint32_t digit, bool live, uint32_
     return had + before;
 }
 
-// Clears the scratch the later launches count in, and copies the keys out.
+// The keys, the first digit's counts of each part, and the bitmap of the
+// tokens that occur (cleared before; null: not wanted).
 __global__ void embed_keys_kernel(TokSource src, int64_t n, int64_t per, uint32_t* __restrict__ keys,
-                                  uint32_t* __restrict__ pos, uint32_t* __restrict__ hist, uint32_t* hist_next,
-                                  int64_t hist_next_words, uint32_t* touched, int64_t touched_words, uint32_t* count,
+                                  uint32_t* __restrict__ pos, uint32_t* __restrict__ hist, uint32_t* touched,
                                   uint32_t* status) {
     __shared__ uint32_t s_hist[kDigits];
     for (int k = threadIdx.x; k < kDigits; k += blockDim.x) s_hist[k] = 0;
-    const int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, gs = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t k = g0; k < hist_next_words; k += gs) hist_next[k] = 0;
-    for (int64_t k = g0; k < touched_words; k += gs) touched[k] = 0;
-    if (g0 == 0) *count = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * per, hi = min(n, lo + per);
     for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
@@ -172,18 +189,18 @@ __global__ void embed_keys_kernel(TokSource src, int64_t n, int64_t per, uint32_
         keys[i] = k;
         pos[i] = (uint32_t)i;
         atomicAdd(&s_hist[k & (kDigits - 1)], 1u);
+        if (touched) atomicOr(touched + (k >> 5), 1u << (k & 31));
     }
     __syncthreads();
     for (int k = threadIdx.x; k < kDigits; k += blockDim.x) hist[(int64_t)blockIdx.x * kDigits + k] = s_hist[k];
 }
 
-// One pass: stable scatter by the digit at `shift`.  hist_next (nullable):
-// counts of the next digit per part of the output.  touched (last pass):
-// bitmap of the tokens that occur.
+// One pass: stable scatter by the digit at `shift`.  hist_next (nullable,
+// cleared before): counts of the next digit per part of the output.
 __global__ void __launch_bounds__(kSortThreads)
 embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, int64_t per,
                      int shift, const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
-                     uint32_t* __restrict__ pos_out, uint32_t* hist_next, uint32_t* touched) {
+                     uint32_t* __restrict__ pos_out, uint32_t* hist_next) {
     __shared__ uint32_t s_base[kDigits];                   // where this part's next element of a digit goes
     __shared__ uint32_t s_cnt[kSortWarps][kDigits];
     __shared__ uint32_t s_scan[kSortWarps];
@@ -250,7 +267,6 @@ embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restri
                 if (hist_next)
                     atomicAdd(hist_next + (to / per) * kDigits + ((key[k] >> (shift + kDigitBits)) & (kDigits - 1)),
                               1u);
-                if (touched) atomicOr(touched + (key[k] >> 5), 1u << (key[k] & 31));
             }
         }
     }
@@ -359,9 +375,8 @@ struct EmbedGrad {
     float scale;
     float* d_E;
     float* part;                  // [n_pieces][2][d]: a piece's first run when it began earlier, its last when it goes on
-    uint32_t* cut;                // pieces whose last run begins there and goes on
+    uint4* cut;                   // runs that a piece's edge cuts: piece where it begins, pieces it reaches, token
     uint32_t* count;
-    const uint32_t* touched;
 };
 
 template <int EPC>
@@ -380,23 +395,31 @@ __device__ __forceinline__ void put_row(float* to, const float* f, float scale, 
     }
 }
 
-// blocks [0, piece_blocks): pieces, blockDim.y at a time; the rest: zero the
-// rows of dE whose token does not occur
+// The rows of dE whose token does not occur, 32 of them (a word of the bitmap)
+// at a time, a warp to a row.  V rows of d floats are most of what the
+// gradient writes: this runs beside the sort and the sums, on the context's
+// side stream (8 x 4096 tokens, V 128000, d 2560: in the reduction's launch
+// 316 us for the whole call, beside it 258 us).
+constexpr int kFillThreads = 512;
+
+__global__ void __launch_bounds__(kFillThreads) embed_fill_kernel(const uint32_t* __restrict__ touched, uint32_t V, int d,
+                                                                  float* __restrict__ d_E) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (uint32_t w = blockIdx.x; w * 32u < V; w += gridDim.x) {
+        const uint32_t bits = __ldg(touched + w);
+        for (uint32_t r = warp; r < 32 && w * 32 + r < V; r += kFillThreads / 32) {
+            if ((bits >> r) & 1u) continue;
+            float4* row = reinterpret_cast<float4*>(d_E + (int64_t)(w * 32 + r) * d);
+            for (int c = lane; c < d / 4; c += 32) row[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+}
+
 template <typename T, int PIECE, bool ACC>
-__global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh, unsigned piece_blocks) {
+__global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh) {
     constexpr int EPC = Vec<T>::N;
     extern __shared__ uint32_t s_mem[];
     const int cpr = p.d / EPC;
-    if (blockIdx.x >= piece_blocks) {
-        const int64_t nb = gridDim.x - piece_blocks;
-        const int vec = p.d / 4;
-        for (int64_t v = (int64_t)(blockIdx.x - piece_blocks) * blockDim.y + threadIdx.y; v < p.V; v += nb * blockDim.y) {
-            if ((__ldg(p.touched + (v >> 5)) >> (v & 31)) & 1u) continue;
-            float4* row = reinterpret_cast<float4*>(p.d_E + v * p.d);
-            for (int c = threadIdx.x; c < vec; c += blockDim.x) row[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        return;
-    }
     const int64_t piece = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     // keys of the piece with one neighbour on each side (kNone outside the list), and its positions
     constexpr uint32_t kNone = 0xffffffffu;
@@ -413,8 +436,24 @@ __global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh, unsig
     const int len = (int)min((int64_t)PIECE, p.n - i0);
     const bool enters = s_key[0] == s_key[1];                    // the first run began before this piece
     const bool leaves = s_key[len] == s_key[len + 1];            // the last run goes on behind it
-    if (threadIdx.x == 0 && leaves && s_key[len] < p.V && !(enters && s_key[1] == s_key[len]))
-        p.cut[atomicAdd(p.count, 1u)] = (uint32_t)piece;
+    if (threadIdx.x == 0 && leaves && s_key[len] < p.V && !(enters && s_key[1] == s_key[len])) {
+        // the first piece behind this one that does not begin with the run's token: most runs reach one
+        // piece further, so the step doubles from there before the search halves it
+        const uint32_t key = s_key[len];
+        int64_t lo = piece + 1, hi = piece + 2, step = 1;
+        while (hi < p.n_pieces && p.keys[hi * PIECE] == key) {
+            lo = hi;
+            hi += step;
+            step <<= 1;
+        }
+        hi = min(hi, p.n_pieces);
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (p.keys[mid * PIECE] == key) lo = mid;
+            else hi = mid;
+        }
+        p.cut[atomicAdd(p.count, 1u)] = make_uint4((uint32_t)piece, (uint32_t)(hi - piece), key, 0u);
+    }
     float* part = p.part + piece * 2 * p.d;
     for (int c = threadIdx.x; c < cpr; c += blockDim.x) {
         float acc[EPC];
@@ -461,33 +500,24 @@ __global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh, unsig
     }
 }
 
-// The cut runs: a CTA takes 128 columns of one run; its eight warps sum
-// contiguous eighths of the run's parts, which are then added in order.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinCols = 128;
+// The cut runs: a CTA takes 512 columns of one run; its two halves sum the
+// first and the second half of the run's parts, which are then added.
+constexpr int kJoinHalf = 128;
+constexpr int kJoinCols = kJoinHalf * 4;
 
 template <int PIECE, bool ACC>
-__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(EmbedGrad p) {
-    __shared__ float4 s_sum[kJoinWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(2 * kJoinHalf) embed_join_kernel(EmbedGrad p) {
+    __shared__ float4 s_sum[kJoinHalf];
+    const int t = threadIdx.x & (kJoinHalf - 1), half = threadIdx.x / kJoinHalf;
     const int slices = (p.d + kJoinCols - 1) / kJoinCols;
     const int64_t work = (int64_t)*p.count * slices;
     for (int64_t u = blockIdx.x; u < work; u += gridDim.x) {
-        const int64_t p0 = p.cut[u / slices];
-        const int col = (int)(u % slices) * kJoinCols + lane * 4;
-        const uint32_t key = p.keys[p0 * PIECE + PIECE - 1];
-        // the last piece the run reaches: pieces after p0 that begin with its token
-        int64_t lo = p0 + 1, hi = p.n_pieces;              // first piece in (p0, n_pieces) that does not
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (p.keys[mid * PIECE] == key) lo = mid + 1;
-            else hi = mid;
-        }
-        const int64_t m = lo - p0;                         // parts: p0's last run, then the first runs of m - 1 pieces
-        const int64_t per = (m + kJoinWarps - 1) / kJoinWarps;
+        const uint4 run = p.cut[u / slices];
+        const int64_t p0 = run.x, m = run.y;               // parts: p0's last run, then the first runs of m - 1 pieces
+        const int col = (int)(u % slices) * kJoinCols + t * 4;
+        const int64_t a = half ? (m + 1) / 2 : 0, b = half ? m : (m + 1) / 2;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < p.d) {
-            const int64_t a = warp * per, b = min(m, a + per);
 #pragma unroll 8
             for (int64_t k = a; k < b; ++k) {
                 const float4 x = *reinterpret_cast<const float4*>(p.part + (p0 + k) * 2 * p.d + (k == 0 ? p.d : 0) + col);
@@ -497,18 +527,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(EmbedGrad p
                 acc.w += x.w;
             }
         }
-        s_sum[warp][lane] = acc;
+        if (half) s_sum[t] = acc;
         __syncthreads();
-        if (warp == 0 && col < p.d) {
-            for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 x = s_sum[w][lane];
-                acc.x += x.x;
-                acc.y += x.y;
-                acc.z += x.z;
-                acc.w += x.w;
-            }
-            const float f[4] = {acc.x, acc.y, acc.z, acc.w};
-            put_row<4>(p.d_E + (int64_t)key * p.d + col, f, p.scale, ACC);
+        if (!half && col < p.d) {
+            const float4 x = s_sum[t];
+            const float f[4] = {acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w};
+            put_row<4>(p.d_E + (int64_t)run.z * p.d + col, f, p.scale, ACC);
         }
         __syncthreads();
     }
@@ -535,8 +559,10 @@ struct EmbedWs {
     uint32_t* hist[2];
     uint32_t* touched;
     uint32_t* count;
-    uint32_t* cut;
+    uint4* cut;
     float* part;
+    void* clear;
+    size_t clear_bytes[2];      // with the bitmap, and without (accumulating calls)
     int64_t hist_words, touched_words, n_pieces;
     int piece;
     size_t bytes;
@@ -557,14 +583,21 @@ EmbedWs embed_carve(const engram_ctx* c, void* base, int64_t n) {
     if (n > kSortSmall) {
         const int64_t per = sort_part(n);
         w.hist_words = (n + per - 1) / per * kDigits;
-        for (int k = 0; k < 2; ++k) w.hist[k] = reinterpret_cast<uint32_t*>(take((size_t)w.hist_words * 4));
+        w.hist[0] = reinterpret_cast<uint32_t*>(take((size_t)w.hist_words * 4));
     }
+    // one clear covers the second pass's counts, the run count and the bitmap
+    char* const cleared = p;
+    if (n > kSortSmall) w.hist[1] = reinterpret_cast<uint32_t*>(take((size_t)w.hist_words * 4));
+    w.count = reinterpret_cast<uint32_t*>(take(4));
+    const size_t no_map = (size_t)(p - cleared);
     w.touched_words = ((int64_t)c->cfg.vocab + 1 + 31) / 32;
     w.touched = reinterpret_cast<uint32_t*>(take((size_t)w.touched_words * 4));
-    w.count = reinterpret_cast<uint32_t*>(take(4));
+    w.clear = cleared;
+    w.clear_bytes[0] = (size_t)(p - cleared);
+    w.clear_bytes[1] = no_map;
     w.piece = piece_of(n, c->num_sms);
     w.n_pieces = (n + w.piece - 1) / w.piece;
-    w.cut = reinterpret_cast<uint32_t*>(take((size_t)w.n_pieces * 4));
+    w.cut = reinterpret_cast<uint4*>(take((size_t)w.n_pieces * 16));
     w.part = reinterpret_cast<float*>(take((size_t)w.n_pieces * 2 * c->cfg.hidden * 4));
     w.bytes = (size_t)(p - static_cast<char*>(base));
     return w;
@@ -575,10 +608,8 @@ cudaError_t launch_reduce(const engram_ctx* c, const EmbedGrad& p, const void* d
     const RowGeo g = row_geo(p.d / Vec<T>::N);
     const dim3 block(g.tpr, g.rb);
     const unsigned pieces = (unsigned)((p.n_pieces + g.rb - 1) / g.rb);
-    unsigned fill = 0;
-    if (!ACC) fill = (unsigned)std::min<int64_t>(((int64_t)p.V + g.rb - 1) / g.rb, (int64_t)c->num_sms * 16);
     const size_t smem = (size_t)g.rb * (2 * PIECE + 2) * 4;
-    embed_reduce_kernel<T, PIECE, ACC><<<pieces + fill, block, smem, s>>>(p, static_cast<const T*>(dh), pieces);
+    embed_reduce_kernel<T, PIECE, ACC><<<pieces, block, smem, s>>>(p, static_cast<const T*>(dh));
     return cudaGetLastError();
 }
 
@@ -592,7 +623,7 @@ cudaError_t reduce_and_join(engram_ctx* c, const EmbedGrad& p, const void* dh, c
     prof_begin(c, s, "embed_join");
     const int slices = (p.d + kJoinCols - 1) / kJoinCols;
     const unsigned blocks = (unsigned)std::min<int64_t>(p.n_pieces * slices, (int64_t)c->num_sms * 8);
-    embed_join_kernel<PIECE, ACC><<<blocks, kJoinWarps * 32, 0, s>>>(p);
+    embed_join_kernel<PIECE, ACC><<<blocks, 2 * kJoinHalf, 0, s>>>(p);
     prof_end(c, s);
     return cudaGetLastError();
 }
@@ -670,34 +701,52 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     const int64_t touched_words = accumulate ? 0 : w.touched_words;
     int at = 0;
     cudaError_t e = cudaSuccess;
+    // the untouched rows are cleared on the side stream as soon as the bitmap stands
+    auto fork_fill = [&]() {
+        if (accumulate || e != cudaSuccess) return;
+        e = cudaEventRecord(c->aux_ev[0], s);
+        if (e == cudaSuccess) e = cudaStreamWaitEvent(c->aux, c->aux_ev[0], 0);
+        if (e != cudaSuccess) return;
+        prof_begin(c, c->aux, "embed_fill");
+        const unsigned blocks = (unsigned)std::min<int64_t>((V + 31) / 32, (int64_t)c->num_sms * 2);
+        embed_fill_kernel<<<blocks, kFillThreads, 0, c->aux>>>(w.touched, (uint32_t)V, d, d_E);
+        prof_end(c, c->aux);
+        e = cudaEventRecord(c->aux_ev[1], c->aux);
+    };
     prof_begin(c, s, "embed_sort");
     if (n <= kSortSmall) {
         embed_sort_small_kernel<<<1, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
                                                             touched_words, w.count, c->d_status);
+        prof_end(c, s);
+        fork_fill();
     } else {
         const int64_t per = sort_part(n);
         const unsigned parts = (unsigned)((n + per - 1) / per);
-        embed_keys_kernel<<<parts, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], w.hist[1],
-                                                         w.hist_words, touched, touched_words, w.count, c->d_status);
-        for (int p = 0; p < passes; ++p) {
+        e = cudaMemsetAsync(w.clear, 0, w.clear_bytes[accumulate ? 1 : 0], s);
+        if (e == cudaSuccess)
+            embed_keys_kernel<<<parts, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], touched, c->d_status);
+        prof_end(c, s);
+        fork_fill();
+        prof_begin(c, s, "embed_sort");
+        for (int p = 0; p < passes && e == cudaSuccess; ++p) {
             const bool last = p + 1 == passes;
-            // the counts of pass p + 1 go where those of pass p - 1 were: cleared here from the third pass on
+            // the counts of pass p + 1 go where those of pass p - 1 were
             if (p > 0 && !last) e = cudaMemsetAsync(w.hist[at ^ 1], 0, (size_t)w.hist_words * 4, s);
             if (e != cudaSuccess) break;
             embed_scatter_kernel<<<parts, kSortThreads, 0, s>>>(w.keys[at], w.pos[at], n, per, p * kDigitBits, w.hist[at],
-                                                                w.keys[at ^ 1], w.pos[at ^ 1], last ? nullptr : w.hist[at ^ 1],
-                                                                last ? touched : nullptr);
+                                                                w.keys[at ^ 1], w.pos[at ^ 1], last ? nullptr : w.hist[at ^ 1]);
             at ^= 1;
         }
+        prof_end(c, s);
     }
-    prof_end(c, s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("embedding gradient sort launches", e);
-    const EmbedGrad p{w.keys[at], w.pos[at], n, w.n_pieces, (uint32_t)V, d, scale, d_E, w.part, w.cut, w.count, w.touched};
+    const EmbedGrad p{w.keys[at], w.pos[at], n, w.n_pieces, (uint32_t)V, d, scale, d_E, w.part, w.cut, w.count};
     if (w.piece == kPieceLong)
         e = accumulate ? reduce_and_join<kPieceLong, true>(c, p, d_h, s) : reduce_and_join<kPieceLong, false>(c, p, d_h, s);
     else
         e = accumulate ? reduce_and_join<kPieceShort, true>(c, p, d_h, s) : reduce_and_join<kPieceShort, false>(c, p, d_h, s);
+    if (e == cudaSuccess && !accumulate) e = cudaStreamWaitEvent(s, c->aux_ev[1], 0);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("embedding gradient launches", e);
 }
 
