@@ -248,11 +248,13 @@ class Engram:
         B, T, stride = self._want_tokens(tok, t_begin)
         n, d = B * (T - t_begin), self.cfg.hidden
         self._want("E", E, (self.cfg.vocab, d), self.dtype)
-        with _on_stream(stream):
-            h = torch.empty(n, d, dtype=self.dtype, device=self.device) if out is None else out
-        self._want("out", h, (n, d), self.dtype)
-        engram_embed(self.ctx, tok, B, T, stride, t_begin, E, scale, h, stream)
-        return h
+        if out is None:
+            with _on_stream(stream):
+                out = torch.empty(n, d, dtype=E.dtype, device=self.device)
+        else:
+            self._want("out", out, (n, d), E.dtype)
+        engram_embed(self.ctx, tok, B, T, stride, t_begin, E, scale, out, stream)
+        return out
 
     def embed_grad(self, tok, d_h, *, t_begin: int = 0, scale: float = 1.0, out=None, accumulate: bool = False,
                    stream=None):
@@ -266,13 +268,16 @@ class Engram:
             raise ValueError("accumulate needs the gradient to add to (out)")
         if n > 1 << 24:
             raise ValueError(f"{n} rows, at most 2^24 in one call")
+        V = self.cfg.vocab
+        if out is not None:
+            self._want("out", out, (V, d), torch.float32)
         with _on_stream(stream):
-            d_E = torch.empty(self.cfg.vocab, d, dtype=torch.float32, device=self.device) if out is None else out
+            if out is None:
+                out = torch.empty(V, d, dtype=torch.float32, device=self.device)
             need = engram_embed_grad_workspace_bytes(self.ctx, n)
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self._want("out", d_E, (self.cfg.vocab, d), torch.float32)
-        engram_embed_grad(self.ctx, tok, B, T, stride, t_begin, d_h, scale, d_E, accumulate, ws, need, stream)
-        return d_E
+        engram_embed_grad(self.ctx, tok, B, T, stride, t_begin, d_h, scale, out, accumulate, ws, need, stream)
+        return out
 
     def add_norm(self, x, res=None, *, gain=None, sum: bool = True, y: bool = True, q: bool = False,
                  rstd: bool = False, stream=None) -> NormOut:
@@ -288,11 +293,11 @@ class Engram:
         if gain is not None:
             self._want("gain", gain, (d,), torch.float32)
         with _on_stream(stream):
-            def new(on, *shape, dtype=self.dtype):
-                return torch.empty(*shape, dtype=dtype, device=self.device) if on else None
-            o = NormOut(new(sum, n, d), new(y, n, d), new(q, n, d, dtype=torch.float8_e4m3fn),
-                        new(q, n, dtype=torch.float32), new(rstd, n, dtype=torch.float32))
-        engram_add_norm(self.ctx, x, res, n, gain, o.sum, o.y, o.q, o.q_scale, o.rstd, stream)
+            o = NormOut(torch.empty_like(x) if sum else None, torch.empty_like(x) if y else None,
+                        torch.empty_like(x, dtype=torch.float8_e4m3fn) if q else None,
+                        torch.empty(n, dtype=torch.float32, device=self.device) if q else None,
+                        torch.empty(n, dtype=torch.float32, device=self.device) if rstd else None)
+        engram_add_norm(self.ctx, x, res, n, gain, *o, stream)
         return o
 
     def add_norm_grad(self, d_y, sum, rstd, *, gain=None, d_sum=None, need_gain: bool = True, stream=None):

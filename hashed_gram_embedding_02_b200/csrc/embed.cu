@@ -22,7 +22,7 @@
 //      takes half of the batch costs nothing extra.
 //   3. join: the parts of each cut run, in order.
 // Meanwhile the rows of the tokens that do not occur are cleared on the
-// context's side stream.
+// context's side stream (a small dE is cleared whole by the first launch).
 // The order of every sum depends on the tokens alone.
 #include <algorithm>
 
@@ -154,6 +154,22 @@ constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallIpt = 4;
 constexpr int kSortSmall = kSmallThreads * kSmallIpt;      // 2048
 constexpr int64_t kMaxEmbedRows = (int64_t)1 << 24;
+// Gradients of at most this many bytes are cleared whole: clearing 64 MB takes
+// the 10 us that the side stream's events and launch cost (256 rows, V 4096, d
+// 256: 22 us a call with them, 17 us without).
+constexpr int64_t kClearWhole = (int64_t)64 << 20;
+
+// A small gradient is cleared whole by the extra CTAs of the sort's first
+// launch, ahead of the sums in the stream.
+struct Zero {
+    float4* to;
+    int64_t vecs;
+    // CTA k of `of`
+    __device__ __forceinline__ void run(unsigned k, unsigned of) const {
+        for (int64_t i = (int64_t)k * blockDim.x + threadIdx.x; i < vecs; i += (int64_t)of * blockDim.x)
+            to[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+};
 
 // tokens outside [0, V) sort behind all others as V
 __device__ __forceinline__ uint32_t sort_key(const TokSource& src, int64_t i, uint32_t* status) {
@@ -179,8 +195,12 @@ __device__ __forceinline__ uint32_t warp_rank(uint32_t digit, bool live, uint32_
 // tokens that occur (cleared before; null: not wanted).
 __global__ void embed_keys_kernel(TokSource src, int64_t n, int64_t per, uint32_t* __restrict__ keys,
                                   uint32_t* __restrict__ pos, uint32_t* __restrict__ hist, uint32_t* touched,
-                                  uint32_t* status) {
+                                  unsigned parts, Zero zero, uint32_t* status) {
     __shared__ uint32_t s_hist[kDigits];
+    if (blockIdx.x >= parts) {
+        zero.run(blockIdx.x - parts, gridDim.x - parts);
+        return;
+    }
     for (int k = threadIdx.x; k < kDigits; k += blockDim.x) s_hist[k] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * per, hi = min(n, lo + per);
@@ -276,7 +296,11 @@ embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restri
 __global__ void __launch_bounds__(kSmallThreads)
 embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__ keys_out,
                         uint32_t* __restrict__ pos_out, uint32_t* touched, int64_t touched_words, uint32_t* count,
-                        uint32_t* status) {
+                        Zero zero, uint32_t* status) {
+    if (blockIdx.x > 0) {
+        zero.run(blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
     __shared__ uint32_t s_key[kSortSmall];
     __shared__ uint16_t s_pos[kSortSmall];
     __shared__ uint16_t s_cnt[kSmallWarps][kDigits];
@@ -562,7 +586,7 @@ struct EmbedWs {
     uint4* cut;
     float* part;
     void* clear;
-    size_t clear_bytes[2];      // with the bitmap, and without (accumulating calls)
+    size_t clear_bytes[2];      // with the bitmap, and without
     int64_t hist_words, touched_words, n_pieces;
     int piece;
     size_t bytes;
@@ -697,13 +721,18 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     EmbedWs w = embed_carve(c, workspace, n);
     const TokSource src{tok, tok_stride, t_begin, T - t_begin, c->cfg.vocab};
     const int passes = sort_passes(c->cfg.vocab);
-    uint32_t* touched = accumulate ? nullptr : w.touched;
-    const int64_t touched_words = accumulate ? 0 : w.touched_words;
+    // what is not summed is cleared: a small dE whole, by the sort's launch; of a large one the rows of the
+    // tokens that do not occur, beside the sort and the sums
+    const bool whole = !accumulate && V * d * 4 <= kClearWhole, beside = !accumulate && !whole;
+    const Zero zero{reinterpret_cast<float4*>(d_E), whole ? V * d / 4 : 0};
+    const unsigned zero_ctas = whole ? (unsigned)std::min<int64_t>((zero.vecs + kSortThreads - 1) / kSortThreads, (int64_t)c->num_sms * 4) : 0;
+    uint32_t* touched = beside ? w.touched : nullptr;
+    const int64_t touched_words = beside ? w.touched_words : 0;
     int at = 0;
     cudaError_t e = cudaSuccess;
     // the untouched rows are cleared on the side stream as soon as the bitmap stands
     auto fork_fill = [&]() {
-        if (accumulate || e != cudaSuccess) return;
+        if (!beside || e != cudaSuccess) return;
         e = cudaEventRecord(c->aux_ev[0], s);
         if (e == cudaSuccess) e = cudaStreamWaitEvent(c->aux, c->aux_ev[0], 0);
         if (e != cudaSuccess) return;
@@ -715,16 +744,17 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     };
     prof_begin(c, s, "embed_sort");
     if (n <= kSortSmall) {
-        embed_sort_small_kernel<<<1, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
-                                                            touched_words, w.count, c->d_status);
+        embed_sort_small_kernel<<<1 + zero_ctas, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
+                                                                        touched_words, w.count, zero, c->d_status);
         prof_end(c, s);
         fork_fill();
     } else {
         const int64_t per = sort_part(n);
         const unsigned parts = (unsigned)((n + per - 1) / per);
-        e = cudaMemsetAsync(w.clear, 0, w.clear_bytes[accumulate ? 1 : 0], s);
+        e = cudaMemsetAsync(w.clear, 0, w.clear_bytes[beside ? 0 : 1], s);
         if (e == cudaSuccess)
-            embed_keys_kernel<<<parts, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], touched, c->d_status);
+            embed_keys_kernel<<<parts + zero_ctas, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], touched,
+                                                                         parts, zero, c->d_status);
         prof_end(c, s);
         fork_fill();
         prof_begin(c, s, "embed_sort");
@@ -746,7 +776,7 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
         e = accumulate ? reduce_and_join<kPieceLong, true>(c, p, d_h, s) : reduce_and_join<kPieceLong, false>(c, p, d_h, s);
     else
         e = accumulate ? reduce_and_join<kPieceShort, true>(c, p, d_h, s) : reduce_and_join<kPieceShort, false>(c, p, d_h, s);
-    if (e == cudaSuccess && !accumulate) e = cudaStreamWaitEvent(s, c->aux_ev[1], 0);
+    if (e == cudaSuccess && beside) e = cudaStreamWaitEvent(s, c->aux_ev[1], 0);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("embedding gradient launches", e);
 }
 
