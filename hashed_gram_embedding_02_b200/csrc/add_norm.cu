@@ -131,43 +131,43 @@ __global__ void __launch_bounds__(kMaxTpr) add_norm_kernel(const T* x, const T* 
     const float r = rsqrtf(ss / (float)(cpr * EPC) + eps);
     if (rstd && tid == 0) rstd[row] = r;
     if (!y && !q) return;
+    // p = g * s; y = p * r, and the codes y / c = 448 p / max |p| without r, so that a code's value has
+    // three roundings behind it
     uint32_t amax = 0;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = tid + k * blockDim.x;
         if (c < cpr) {
-            float g[EPC];
             if (gain) {
 #pragma unroll
                 for (int j = 0; j < EPC; j += 4) {
                     const float4 v = __ldg(reinterpret_cast<const float4*>(gain + c * EPC + j));
-                    g[j] = v.x; g[j + 1] = v.y; g[j + 2] = v.z; g[j + 3] = v.w;
+                    f[k][j] *= v.x; f[k][j + 1] *= v.y; f[k][j + 2] *= v.z; f[k][j + 3] *= v.w;
                 }
             }
+            float o[EPC];
 #pragma unroll
             for (int j = 0; j < EPC; ++j) {
-                f[k][j] *= r;
-                if (gain) f[k][j] *= g[j];
+                o[j] = f[k][j] * r;
                 amax = max(amax, abs_bits(f[k][j]));
             }
-            if (y) Vec<T>::store(y + (base + c) * EPC, f[k]);
+            if (y) Vec<T>::store(y + (base + c) * EPC, o);
         }
     }
     if (!q) return;
-    amax = row_max(amax, s_max, warps, warp, lane);
-    const float c_row = __uint_as_float(amax) / kE4M3Max;
-    if (tid == 0) q_scale[row] = c_row;
-    // one reciprocal per row; a scale whose reciprocal would overflow divides instead, and a row of zeros
+    const float top = __uint_as_float(row_max(amax, s_max, warps, warp, lane));
+    if (tid == 0) q_scale[row] = top * r / kE4M3Max;
+    // one reciprocal per row; a row whose reciprocal would overflow divides instead, and a row of zeros
     // (scale 0) has codes 0
-    const bool tiny = c_row < 1e-37f;
-    const float inv = 1.f / c_row;
+    const bool tiny = top < 1e-35f;
+    const float inv = kE4M3Max / top;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
         const int c = tid + k * blockDim.x;
         if (c < cpr) {
             float o[EPC];
 #pragma unroll
-            for (int j = 0; j < EPC; ++j) o[j] = tiny ? (c_row > 0.f ? f[k][j] / c_row : 0.f) : f[k][j] * inv;
+            for (int j = 0; j < EPC; ++j) o[j] = tiny ? (top > 0.f ? f[k][j] / top * kE4M3Max : 0.f) : f[k][j] * inv;
             store_e4m3<EPC>(q + (base + c) * EPC, o);
         }
     }

@@ -21,8 +21,8 @@
 //      the same for every piece however often a token occurs, so a token that
 //      takes half of the batch costs nothing extra.
 //   3. join: the parts of each cut run, in order.
-// Meanwhile the rows of the tokens that do not occur are cleared on the
-// context's side stream (a small dE is cleared whole by the first launch).
+// Between 1 and 2 the rows of the tokens that do not occur are cleared (a small
+// dE is cleared whole by the sort's first launch).
 // The order of every sum depends on the tokens alone.
 #include <algorithm>
 
@@ -155,8 +155,8 @@ constexpr int kSmallIpt = 4;
 constexpr int kSortSmall = kSmallThreads * kSmallIpt;      // 2048
 constexpr int64_t kMaxEmbedRows = (int64_t)1 << 24;
 // Gradients of at most this many bytes are cleared whole: clearing 64 MB takes
-// the 10 us that the side stream's events and launch cost (256 rows, V 4096, d
-// 256: 22 us a call with them, 17 us without).
+// 9 us, the bitmap and a launch of their own cost as much (256 rows, V 4096, d
+// 256: 20 us a call with them, 17 us without).
 constexpr int64_t kClearWhole = (int64_t)64 << 20;
 
 // A small gradient is cleared whole by the extra CTAs of the sort's first
@@ -397,45 +397,58 @@ struct EmbedGrad {
     uint32_t V;
     int d;
     float scale;
+    bool wide;                    // rows of dE are 32-byte aligned (d is a multiple of 8)
     float* d_E;
     float* part;                  // [n_pieces][2][d]: a piece's first run when it began earlier, its last when it goes on
     uint4* cut;                   // runs that a piece's edge cuts: piece where it begins, pieces it reaches, token
     uint32_t* count;
 };
 
+// EPC floats of a row.  A thread's eight go out as one 32-byte store where
+// the rows are aligned for it: as two of 16 bytes, each warp store would fill
+// half of its sectors.
 template <int EPC>
-__device__ __forceinline__ void put_row(float* to, const float* f, float scale, bool accumulate) {
-#pragma unroll
-    for (int k = 0; k < EPC; k += 4) {
-        float4 o = make_float4(scale * f[k], scale * f[k + 1], scale * f[k + 2], scale * f[k + 3]);
-        if (accumulate) {
-            const float4 was = *reinterpret_cast<const float4*>(to + k);
-            o.x += was.x;
-            o.y += was.y;
-            o.z += was.z;
-            o.w += was.w;
-        }
-        *reinterpret_cast<float4*>(to + k) = o;
+__device__ __forceinline__ void store_row(float* to, const float* f, bool wide) {
+    if (EPC == 8 && wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+                     "f"(f[3]), "f"(f[EPC - 4]), "f"(f[EPC - 3]), "f"(f[EPC - 2]), "f"(f[EPC - 1])
+                     : "memory");
+        return;
     }
+#pragma unroll
+    for (int k = 0; k < EPC; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+}
+
+template <int EPC>
+__device__ __forceinline__ void put_row(float* to, const float* f, float scale, bool accumulate, bool wide) {
+    float o[EPC];
+#pragma unroll
+    for (int k = 0; k < EPC; ++k) o[k] = scale * f[k];
+    if (accumulate) {
+#pragma unroll
+        for (int k = 0; k < EPC; k += 4) {
+            const float4 was = *reinterpret_cast<const float4*>(to + k);
+            o[k] += was.x; o[k + 1] += was.y; o[k + 2] += was.z; o[k + 3] += was.w;
+        }
+    }
+    store_row<EPC>(to, o, wide);
 }
 
 // The rows of dE whose token does not occur, 32 of them (a word of the bitmap)
-// at a time, a warp to a row.  V rows of d floats are most of what the
-// gradient writes: this runs beside the sort and the sums, on the context's
-// side stream (8 x 4096 tokens, V 128000, d 2560: in the reduction's launch
-// 316 us for the whole call, beside it 258 us).
+// to a CTA, a warp to a row.  V rows of d floats are most of what the gradient
+// writes (8 x 4096 tokens, V 128000, d 2560: 173 us, 7.1 TB/s; CTAs that loop
+// over the words reach 197 us, and clearing in the launch of the sums or on a
+// side stream starves the sums: 316 and 292 us for a call, so 276 us).
 constexpr int kFillThreads = 512;
 
 __global__ void __launch_bounds__(kFillThreads) embed_fill_kernel(const uint32_t* __restrict__ touched, uint32_t V, int d,
                                                                   float* __restrict__ d_E) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (uint32_t w = blockIdx.x; w * 32u < V; w += gridDim.x) {
-        const uint32_t bits = __ldg(touched + w);
-        for (uint32_t r = warp; r < 32 && w * 32 + r < V; r += kFillThreads / 32) {
-            if ((bits >> r) & 1u) continue;
-            float4* row = reinterpret_cast<float4*>(d_E + (int64_t)(w * 32 + r) * d);
-            for (int c = lane; c < d / 4; c += 32) row[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    const uint32_t w = blockIdx.x, bits = __ldg(touched + w);
+    for (uint32_t r = warp; r < 32 && w * 32 + r < V; r += kFillThreads / 32) {
+        if ((bits >> r) & 1u) continue;
+        float4* row = reinterpret_cast<float4*>(d_E + (int64_t)(w * 32 + r) * d);
+        for (int c = lane; c < d / 4; c += 32) row[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -503,17 +516,9 @@ __global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh) {
                 if (e + 1 == len || s_key[e + 2] != key) {
                     // the end of a run, or of the piece
                     if (key < p.V) {
-                        if (first && enters) {
-#pragma unroll
-                            for (int k = 0; k < EPC; k += 4)
-                                *reinterpret_cast<float4*>(part + c * EPC + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
-                        } else if (e + 1 == len && leaves) {
-#pragma unroll
-                            for (int k = 0; k < EPC; k += 4)
-                                *reinterpret_cast<float4*>(part + p.d + c * EPC + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
-                        } else {
-                            put_row<EPC>(p.d_E + (int64_t)key * p.d + c * EPC, acc, p.scale, ACC);
-                        }
+                        if (first && enters) store_row<EPC>(part + c * EPC, acc, true);
+                        else if (e + 1 == len && leaves) store_row<EPC>(part + p.d + c * EPC, acc, true);
+                        else put_row<EPC>(p.d_E + (int64_t)key * p.d + c * EPC, acc, p.scale, ACC, p.wide);
                     }
 #pragma unroll
                     for (int k = 0; k < EPC; ++k) acc[k] = 0.f;
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(2 * kJoinHalf) embed_join_kernel(EmbedGrad p) 
         if (!half && col < p.d) {
             const float4 x = s_sum[t];
             const float f[4] = {acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w};
-            put_row<4>(p.d_E + (int64_t)run.z * p.d + col, f, p.scale, ACC);
+            put_row<4>(p.d_E + (int64_t)run.z * p.d + col, f, p.scale, ACC, false);
         }
         __syncthreads();
     }
@@ -722,42 +727,25 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     const TokSource src{tok, tok_stride, t_begin, T - t_begin, c->cfg.vocab};
     const int passes = sort_passes(c->cfg.vocab);
     // what is not summed is cleared: a small dE whole, by the sort's launch; of a large one the rows of the
-    // tokens that do not occur, beside the sort and the sums
-    const bool whole = !accumulate && V * d * 4 <= kClearWhole, beside = !accumulate && !whole;
+    // tokens that do not occur
+    const bool whole = !accumulate && V * d * 4 <= kClearWhole, rest = !accumulate && !whole;
     const Zero zero{reinterpret_cast<float4*>(d_E), whole ? V * d / 4 : 0};
     const unsigned zero_ctas = whole ? (unsigned)std::min<int64_t>((zero.vecs + kSortThreads - 1) / kSortThreads, (int64_t)c->num_sms * 4) : 0;
-    uint32_t* touched = beside ? w.touched : nullptr;
-    const int64_t touched_words = beside ? w.touched_words : 0;
+    uint32_t* touched = rest ? w.touched : nullptr;
+    const int64_t touched_words = rest ? w.touched_words : 0;
     int at = 0;
     cudaError_t e = cudaSuccess;
-    // the untouched rows are cleared on the side stream as soon as the bitmap stands
-    auto fork_fill = [&]() {
-        if (!beside || e != cudaSuccess) return;
-        e = cudaEventRecord(c->aux_ev[0], s);
-        if (e == cudaSuccess) e = cudaStreamWaitEvent(c->aux, c->aux_ev[0], 0);
-        if (e != cudaSuccess) return;
-        prof_begin(c, c->aux, "embed_fill");
-        const unsigned blocks = (unsigned)std::min<int64_t>((V + 31) / 32, (int64_t)c->num_sms * 2);
-        embed_fill_kernel<<<blocks, kFillThreads, 0, c->aux>>>(w.touched, (uint32_t)V, d, d_E);
-        prof_end(c, c->aux);
-        e = cudaEventRecord(c->aux_ev[1], c->aux);
-    };
     prof_begin(c, s, "embed_sort");
     if (n <= kSortSmall) {
         embed_sort_small_kernel<<<1 + zero_ctas, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
                                                                         touched_words, w.count, zero, c->d_status);
-        prof_end(c, s);
-        fork_fill();
     } else {
         const int64_t per = sort_part(n);
         const unsigned parts = (unsigned)((n + per - 1) / per);
-        e = cudaMemsetAsync(w.clear, 0, w.clear_bytes[beside ? 0 : 1], s);
+        e = cudaMemsetAsync(w.clear, 0, w.clear_bytes[rest ? 0 : 1], s);
         if (e == cudaSuccess)
             embed_keys_kernel<<<parts + zero_ctas, kSortThreads, 0, s>>>(src, n, per, w.keys[0], w.pos[0], w.hist[0], touched,
                                                                          parts, zero, c->d_status);
-        prof_end(c, s);
-        fork_fill();
-        prof_begin(c, s, "embed_sort");
         for (int p = 0; p < passes && e == cudaSuccess; ++p) {
             const bool last = p + 1 == passes;
             // the counts of pass p + 1 go where those of pass p - 1 were
@@ -767,16 +755,22 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
                                                                 w.keys[at ^ 1], w.pos[at ^ 1], last ? nullptr : w.hist[at ^ 1]);
             at ^= 1;
         }
+    }
+    prof_end(c, s);
+    if (rest && e == cudaSuccess) {
+        prof_begin(c, s, "embed_fill");
+        const unsigned blocks = (unsigned)((V + 31) / 32);
+        embed_fill_kernel<<<blocks, kFillThreads, 0, s>>>(w.touched, (uint32_t)V, d, d_E);
         prof_end(c, s);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("embedding gradient sort launches", e);
-    const EmbedGrad p{w.keys[at], w.pos[at], n, w.n_pieces, (uint32_t)V, d, scale, d_E, w.part, w.cut, w.count};
+    const EmbedGrad p{w.keys[at], w.pos[at], n, w.n_pieces, (uint32_t)V, d, scale,
+                      (reinterpret_cast<uintptr_t>(d_E) & 31u) == 0, d_E, w.part, w.cut, w.count};
     if (w.piece == kPieceLong)
         e = accumulate ? reduce_and_join<kPieceLong, true>(c, p, d_h, s) : reduce_and_join<kPieceLong, false>(c, p, d_h, s);
     else
         e = accumulate ? reduce_and_join<kPieceShort, true>(c, p, d_h, s) : reduce_and_join<kPieceShort, false>(c, p, d_h, s);
-    if (e == cudaSuccess && beside) e = cudaStreamWaitEvent(s, c->aux_ev[1], 0);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("embedding gradient launches", e);
 }
 
