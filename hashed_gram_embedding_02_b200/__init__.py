@@ -347,6 +347,8 @@ class Engram:
         n, f, a = self._ffn_args(x, Wgu, Wd, act, dt, dt)
         if (x_scale is None or gu_scale is None) if f8 else (x_scale is not None or gu_scale is not None):
             raise ValueError("x_scale and gu_scale go with an FP8 context, and are required there")
+        if save and f8:
+            raise ValueError("save is for the backward, which takes bf16 contexts")
         if f8:
             self._want("x_scale", x_scale, (n,), torch.float32)
             self._want("gu_scale", gu_scale, (2 * f,), torch.float32)

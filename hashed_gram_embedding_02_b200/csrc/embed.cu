@@ -52,7 +52,7 @@ RowGeo row_geo(int cpr) {
         g.tpr = 1;
         while (g.tpr < cpr) g.tpr <<= 1;
     }
-    g.rb = std::max(1, 256 / g.tpr);
+    g.rb = std::min(128, std::max(1, 256 / g.tpr));   // 128 long pieces: 34 KB of keys and positions
     return g;
 }
 

@@ -95,6 +95,7 @@ struct FfnParams {
     const float* col_scale;     // FP8: [2N]
     float* part;                // PART: [splits][M][N] (GLU: [splits][M][2N])
     uint32_t* status;
+    int stall;                  // test hook: CTA 0 announces its first B stage but never loads it
 };
 
 // Bounded wait for the phase with `parity`; false when the CTA aborted or the
@@ -370,7 +371,9 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     const int k0 = kb * KSTEP;
                     const uint32_t a_dst = tiles_u32 + s * stage_bytes;
                     const uint32_t b_dst = a_dst + p.a_bytes;
-                    if (is_a) {
+                    if (p.stall && it == 0 && warp == 2 && blockIdx.x == 0) {
+                        // bounded-wait test: announced above, never loaded
+                    } else if (is_a) {
                         if (AMN) load(&map_a, a_dst + part * (BK * ROWB), m0 + part * 64, k0);
                         else load(&map_a, a_dst, k0, m0);
                     } else if constexpr (BMN) {
@@ -690,11 +693,11 @@ struct Plan {
 //             and its bytes into one SM
 //   all       the weights from HBM
 //   a split   the partial sums written and read back, and the join's launch
-Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
+Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
     Plan best{};
     double best_cost = 1e30;
     const bool pair = M > BM;
-    const int workers = pair ? c->num_sms / 2 : c->num_sms;
+    const int workers = pair ? num_sms / 2 : num_sms;
     const int64_t cols = glu ? 2 * N : N;
     const int step = bmn ? (pair ? 128 : 64) : (pair ? 32 : 16);
     const int a_rows = !pair && !amn ? (int)(M + 7) / 8 * 8 : BM;
@@ -720,6 +723,31 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
         }
     }
     return best;
+}
+
+// The search takes about a microsecond and a call needs each of its plans
+// three times: the last ones of this thread are kept, by their sizes.
+Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
+    struct Entry {
+        int64_t M = -1, N = 0;
+        int kb = 0, num_sms = 0, kind = 0;
+        Plan plan{};
+    };
+    constexpr int kEntries = 16;
+    static thread_local Entry cache[kEntries];
+    static thread_local int next = 0;
+    const int kind = glu | amn << 1 | bmn << 2;
+    for (const Entry& e : cache)
+        if (e.M == M && e.N == N && e.kb == kb && e.num_sms == c->num_sms && e.kind == kind) return e.plan;
+    Entry& e = cache[next];
+    next = (next + 1) % kEntries;
+    e.plan = search_plan(c->num_sms, M, N, kb, glu, amn, bmn);
+    e.M = M;
+    e.N = N;
+    e.kb = kb;
+    e.num_sms = c->num_sms;
+    e.kind = kind;
+    return e.plan;
 }
 
 template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
@@ -959,6 +987,8 @@ engram_status engram_ffn(engram_ctx* c, const void* x, const float* x_scale, int
     }
     p.row_scale = x_scale;
     p.col_scale = gu_scale;
+    p.stall = c->debug_stall;
+    c->debug_stall = 0;
     cudaError_t e = f8 ? product<EPI_GLU, false, false, true>(c, x, d, Wgu, d, n, f, d, p, w.part, "ffn_gate_up_fp8", false, s)
                        : product<EPI_GLU, false, false>(c, x, d, Wgu, d, n, f, d, p, w.part, "ffn_gate_up", false, s);
     if (e != cudaSuccess) return cuda_fail("feed-forward gate/up launch", e);

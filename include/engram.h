@@ -155,7 +155,8 @@ ENGRAM_API engram_status engram_profile_enable(engram_ctx* ctx, int32_t enable);
 ENGRAM_API int32_t engram_profile_read(engram_ctx* ctx, float* ms, const char** names, int32_t max);
 
 /* Test hook for the bounded device waits (failure detection without a
- * fault): the next fused key pass (tcgen05 path) of this context announces
+ * fault): the next fused key pass (tcgen05 path) or feed-forward gate/up
+ * product of this context announces
  * the bytes of its first operand stage in CTA 0 but never loads them, so the
  * MMA warp's wait on that stage runs out after about 2 s.  The kernel then
  * sets ENGRAM_ERR_TIMEOUT, raises its abort flag, drains the copies and MMAs
