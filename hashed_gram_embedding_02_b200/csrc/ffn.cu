@@ -55,11 +55,15 @@ constexpr int TMEM_COLS = 512;
 // rows stage only the rows they have, and a narrow tile only its columns, so
 // that more stages are in flight: the ring's round trip (free slot -> load ->
 // MMA -> free slot) is about 1.4 us, and a stage takes that over the number of
-// stages at least.  A pair's epilogue keeps the last 64 KB for its patches,
-// which leaves five stages of a 256 x 256 tile (with three it is slower, with
-// seven no faster).
+// stages at least.  A pair's epilogue keeps the end of the area for its patches or
+// inputs, which leaves six or four stages of a 256 x 256 tile (with three it is
+// slower, with seven no faster).
 constexpr int TILE_AREA = 7 * 32768;
-constexpr int STAGING = 65536;          // two 4 KB patches for each epilogue warp of a pair
+constexpr int STAGING = EPI_WARPS * 4096;    // a patch for each epilogue warp of a pair
+// DGLU on a pair: two buffers per epilogue warp for 32 columns of its 32 rows'
+// g and u: [g high 2 KB | u high 2 KB | g low 1 KB | u low 1 KB]
+constexpr int IN_BUF = 6144;
+constexpr int IN_AREA = EPI_WARPS * 2 * IN_BUF;
 constexpr int MAX_STAGES = 14;
 constexpr int SMEM_BYTES = TILE_AREA + 1024 + 1024;   // ring | barriers | alignment
 
@@ -69,6 +73,7 @@ struct __align__(8) Barriers {
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
+    uint64_t in[EPI_WARPS][2];     // DGLU on a pair: the warp's input buffers
     uint32_t tmem_base;
     volatile int abort_flag;
     int issued[5];            // stages loaded by each producer warp
@@ -152,22 +157,33 @@ __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t da, uint64_t db, 
 
 // ---------------------------------------------------------------- activation
 
-// act(g) and its factor p = act(g) / g (the logistic function of k(g))
-__device__ __forceinline__ float act_p(float g, int act) {
-    // k = g, or 2 sqrt(2/pi) (g + 0.044715 g^3)
-    const float k = act == ENGRAM_ACT_SILU ? g : g * fmaf(0.0713548163f, g * g, 1.5957691216f);
-    return __fdividef(1.f, 1.f + __expf(-k));
+// p = act(g) / g = 1 / (1 + exp(-k)): k = g, or 2 sqrt(2/pi) (g + 0.044715 g^3)
+// = g k1, with exp(-k) = 2^(-k log2 e) by the hardware's base-2 exponential and
+// reciprocal (2 and 1 ulp; an infinite denominator gives 0).  g2 = g^2, held
+// below 1e4 so that k' stays finite where p is 0 or 1 anyway.
+template <bool GELU>
+__device__ __forceinline__ float act_p(float g, float& g2) {
+    constexpr float kLog2e = 1.4426950409f;
+    float k = -kLog2e * g, e, r;
+    if (GELU) {
+        g2 = fminf(g * g, 1e4f);
+        k = g * fmaf(-0.0713548163f * kLog2e, g2, -1.5957691216f * kLog2e);
+    }
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(k));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 
-// act'(g) = p + g p (1 - p) k'(g)
-__device__ __forceinline__ float act_d(float g, float p, int act) {
-    const float dk = act == ENGRAM_ACT_SILU ? 1.f : fmaf(0.2140644488f, g * g, 1.5957691216f);
-    return fmaf(g * dk * p, 1.f - p, p);
+// act'(g) = p + g p (1 - p) k'(g), gp = g p
+template <bool GELU>
+__device__ __forceinline__ float act_d(float gp, float p, float g2) {
+    if (GELU) gp *= fmaf(0.2140644488f, g2, 1.5957691216f);
+    return fmaf(gp, 1.f - p, p);
 }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) { Vec<__nv_bfloat16>::load(p, f); }
 
-// g and u are kept for the backward as 24 of their 32 bits (half a step 2^-16):
+// g and u are kept for the backward as 24 of their 32 bits:
 // in bf16 their rounding would reach d_x and d_Wgu beside that of dg and du
 // (measured against 64 bits: 3.5e-3 of the norm, with 24 bits 2.4e-3); the
 // lower plane costs a byte per value.  Both planes are blocked as the
@@ -179,15 +195,12 @@ __device__ __forceinline__ int64_t at24(const FfnParams& p, int64_t row, int col
     return ((row >> 5) * (p.N / 4) + col / 8) * 32 + (row & 31);
 }
 
-__device__ __forceinline__ uint32_t round24(float x) {
-    const uint32_t b = __float_as_uint(x);
-    return (b & 0x7fffffffu) > 0x7f800000u ? 0x7fc00000u : b + 0x80u;   // NaN stays NaN
-}
-
+// (cut off, not rounded: reading repeats the low byte below itself, so a value
+// is within one step of 2^-15 and a NaN stays one)
 __device__ __forceinline__ void put24(const FfnParams& p, int64_t at, const float* f) {
     uint32_t b[8], hi[4], lo[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) b[k] = round24(f[k]);
+    for (int k = 0; k < 8; ++k) b[k] = __float_as_uint(f[k]);
 #pragma unroll
     for (int k = 0; k < 4; ++k) hi[k] = __byte_perm(b[2 * k], b[2 * k + 1], 0x7632);
 #pragma unroll
@@ -208,33 +221,35 @@ struct Raw24 {
         const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            // bytes: the high half of h[k / 2] or its low half, then byte k % 4 of the lower plane
-            const uint32_t top = k & 1 ? h[k / 2] & 0xffff0000u : h[k / 2] << 16;
-            f[k] = __uint_as_float(top | ((l[k / 4] >> (8 * (k & 3))) & 0xffu) << 8);
+            // bytes 3, 2 from a half of h, 1 and 0 both byte k % 4 of l
+            f[k] = __uint_as_float(__byte_perm(l[k / 4], h[k / 2], (k & 1 ? 0x7600u : 0x5400u) + 0x11u * (k & 3)));
         }
     }
 };
 
-// Eight columns from c of one row, wherever the sums came from; *_8 leave the
+// Eight columns from c of one row, wherever the sums came from; *8 leave the
 // values to store in their arguments.
+template <bool GELU>
 __device__ __forceinline__ void glu8(const FfnParams& p, int64_t row, int c, float* g, const float* u) {
     if (p.gu_hi) {
         put24(p, at24(p, row, c), g);
         put24(p, at24(p, row, p.N + c), u);
     }
+    float g2;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] *= act_p(g[k], p.act) * u[k];
+    for (int k = 0; k < 8; ++k) g[k] = g[k] * act_p<GELU>(g[k], g2) * u[k];
 }
 
-__device__ __forceinline__ void dglu8(const FfnParams& p, const Raw24& rg, const Raw24& ru, float* dg, float* du) {
-    float g[8], u[8];
+template <bool GELU>
+__device__ __forceinline__ void dglu8(const Raw24& rg, const Raw24& ru, float* dg, float* du) {
+    float g[8], u[8], g2;
     rg.get(g);
     ru.get(u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float da = dg[k], pr = act_p(g[k], p.act);
-        du[k] = da * (g[k] * pr);
-        dg[k] = da * u[k] * act_d(g[k], pr, p.act);
+        const float da = dg[k], pr = act_p<GELU>(g[k], g2), gp = g[k] * pr;
+        du[k] = da * gp;
+        dg[k] = da * u[k] * act_d<GELU>(gp, pr, g2);
     }
 }
 
@@ -253,7 +268,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 
 // AMN / BMN: the operand is MN-major (contraction index = row of its matrix).
 // GLU: B's two column halves are the gate and up rows of the same channels.
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU>
 __global__ void __launch_bounds__(THREADS, 1)
 ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
     constexpr int NCTA = PAIR ? 2 : 1;
@@ -282,6 +297,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             mbar_init(&sb->tempty[a], NCTA * EPI_WARPS);
         }
         mbar_init(&sb->drain, 1);
+        for (int w = 0; w < 2 * EPI_WARPS; ++w) mbar_init(&sb->in[0][0] + w, 1);
         sb->abort_flag = 0;
         for (int w = 0; w < 5; ++w) sb->issued[w] = 0;
         sb->consumed = 0;
@@ -448,16 +464,48 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         // in a patch of shared memory [32 rows][128 bytes] (16-byte chunks
         // swizzled by the row), and the patch goes out four full lines per
         // instruction; by rows, a store touches 32 lines of 16 bytes.
-        constexpr bool STAGED = PAIR && EPI != EPI_PART;
+        constexpr bool BULK = PAIR && EPI == EPI_DGLU;
+        constexpr bool STAGED = PAIR && EPI != EPI_PART && !BULK;
         constexpr int BLK = STAGED ? 64 : 16;
         uint8_t* patch = smem + TILE_AREA - STAGING + (warp - EPI_WARP0) * (STAGING / EPI_WARPS);
-        auto patch_at = [&](int k, int r, int ch) {
-            return reinterpret_cast<uint4*>(patch + k * 4096 + r * 128 + ((ch ^ (r & 7)) << 4));
+        auto patch_at = [&](int r, int ch) {
+            return reinterpret_cast<uint4*>(patch + r * 128 + ((ch ^ (r & 7)) << 4));
         };
         // the warp's k-th chunk of 16 columns
         auto chunk = [&](int k) { return part * BLK + k / (BLK / 16) * (BLK * EPI_PARTS) + k % (BLK / 16) * 16; };
         int tc = 0;
         grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
+        // BULK: 32 columns of g and u at a time, copied by the warp's lane 0 a
+        // block ahead, over tiles too.  Loads into registers keep too few
+        // bytes in flight: the epilogue of 16384 rows, f 6912 alone took 399
+        // us with them, 149 us without, BULK_FIG us with the copies.
+        uint8_t* in_buf = smem + TILE_AREA - IN_AREA + (warp - EPI_WARP0) * 2 * IN_BUF;
+        int in_sent = 0, in_used = 0;
+        // columns of g (and of u) of block b of unit u that this warp reads: 0 where there is nothing
+        auto in_cols = [&](const Where& w, int b) {
+            const int64_t row0 = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
+            return row0 < p.M ? max(0, min(32, p.N - (w.nt * p.bn + b))) : 0;
+        };
+        auto in_copy = [&](const Where& w, int b) {
+            const int cols = in_cols(w, b);
+            if (cols == 0) return;
+            if (lane == 0) {
+                const int64_t row0 = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
+                const int col = w.nt * p.bn + b;
+                uint8_t* to = in_buf + (in_sent & 1) * IN_BUF;
+                uint64_t* bar = &sb->in[warp - EPI_WARP0][in_sent & 1];
+                const uint32_t hi = (uint32_t)cols * 64, lo = (uint32_t)cols * 32;
+                mbar_arrive_expect_tx(bar, 2 * (hi + lo));
+                bulk_g2s(to, p.gu_hi + at24(p, row0, col), hi, bar);
+                bulk_g2s(to + 2048, p.gu_hi + at24(p, row0, p.N + col), hi, bar);
+                bulk_g2s(to + 4096, p.gu_lo + at24(p, row0, col), lo, bar);
+                bulk_g2s(to + 5120, p.gu_lo + at24(p, row0, p.N + col), lo, bar);
+            }
+            ++in_sent;
+        };
+        if constexpr (BULK) {
+            if (unit0 < num_units) in_copy(where(unit0), part * 32);
+        }
         for (int u = unit0; u < num_units; u += step, ++tc) {
             const Where w = where(u);
             const int acc = tc & 1;
@@ -467,7 +515,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             const int width = GLU ? p.bn / 2 : p.bn;       // output columns of the tile
             const int c_tile = w.nt * width;
             // g and u of two chunks are held or in flight, the tile's first ones while its MMAs run
-            Raw24 rg[2][2], ru[2][2];
+            Raw24 rg[2][2], ru[2][2];     // not BULK
             auto fetch = [&](int c, Raw24* fg, Raw24* fu) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -478,7 +526,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     }
                 }
             };
-            if constexpr (EPI == EPI_DGLU) {
+            if constexpr (EPI == EPI_DGLU && !BULK) {
                 fetch(chunk(0), rg[0], ru[0]);
                 fetch(chunk(1), rg[1], ru[1]);
             }
@@ -488,6 +536,68 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             const uint32_t taddr = tmem_base + (uint32_t)(acc * MAX_BN) + ((uint32_t)(q * 32) << 16);
             float rs = 1.f;
             if (F8 && live) rs = __ldg(p.row_scale + row);
+            if constexpr (BULK) {
+                bool in_ok = true;
+#pragma unroll 1
+                for (int b = part * 32; b < p.bn; b += 32 * EPI_PARTS) {
+                    // the next block: of this tile, or the first of the next one
+                    if (b + 32 * EPI_PARTS < p.bn) in_copy(w, b + 32 * EPI_PARTS);
+                    else if (u + step < num_units) in_copy(where(u + step), part * 32);
+                    const int cols = in_cols(w, b);
+                    if (cols == 0) continue;
+                    const uint8_t* from = in_buf + (in_used & 1) * IN_BUF + lane * 16;
+                    in_ok = wait_bounded(&sb->in[warp - EPI_WARP0][in_used & 1], (uint32_t)(in_used >> 1) & 1u, sb, p.status);
+                    if (!__all_sync(0xffffffffu, in_ok)) break;
+                    ++in_used;
+                    uint4 o[4][2];
+#pragma unroll
+                    for (int c16 = 0; c16 < 32; c16 += 16) {
+                        uint32_t x[16];
+                        tmem_ld16(taddr + b + c16, x);
+                        tmem_wait_ld(x);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int g8 = c16 / 8 + h;
+                            Raw24 xg, xu;
+                            xg.hi = *reinterpret_cast<const uint4*>(from + g8 * 512);
+                            xu.hi = *reinterpret_cast<const uint4*>(from + 2048 + g8 * 512);
+                            xg.lo = *reinterpret_cast<const uint2*>(from - lane * 8 + 4096 + g8 * 256);
+                            xu.lo = *reinterpret_cast<const uint2*>(from - lane * 8 + 5120 + g8 * 256);
+                            float f[8], g[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(x[h * 8 + k]);
+                            dglu8<GELU>(xg, xu, f, g);
+                            o[g8][0] = pack8(f);
+                            o[g8][1] = pack8(g);
+                        }
+                    }
+                    // out through the same buffer: [dg | du][32 rows][64 bytes], chunks swizzled by the row pair,
+                    // then two full sectors a row, eight rows per instruction
+                    uint8_t* const out_buf = in_buf + ((in_used - 1) & 1) * IN_BUF;
+                    __syncwarp();
+#pragma unroll
+                    for (int g8 = 0; g8 < 4; ++g8)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<uint4*>(out_buf + k * 2048 + lane * 64 + ((g8 ^ ((lane >> 1) & 3)) << 4)) = o[g8][k];
+                    __syncwarp();
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int r = it * 8 + (lane >> 2), ch = lane & 3;
+                        const int64_t to_row = row - lane + r;
+                        if (to_row < p.M && ch * 8 < cols) {
+                            const uint8_t* at = out_buf + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+                            __nv_bfloat16* to = p.out + to_row * p.ldo + c_tile + b + ch * 8;
+                            *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(at);
+                            *reinterpret_cast<uint4*>(to + p.N) = *reinterpret_cast<const uint4*>(at + 2048);
+                        }
+                    }
+                    // the buffer is read and written before the next copy into it
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (!__all_sync(0xffffffffu, in_ok)) break;
+            }
             // the patch's lane: row r of four, 16-byte chunk lane % 8
             auto each_line = [&](int b0, auto&& f) {
 #pragma unroll
@@ -498,7 +608,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (to_row < p.M && b0 + ch * 8 < width && col < p.N) f(r, ch, to_row, col);
                 }
             };
-            const int nk = STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4 : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
+            const int nk = BULK ? 0 : STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4 : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
 #pragma unroll 1
             for (int k2 = 0; k2 < nk; k2 += 2) {
 #pragma unroll
@@ -507,7 +617,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (b0 >= width) break;
                     if (STAGED && EPI == EPI_OUT && p.res && k % 4 == 0) {
                         each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
-                            *patch_at(0, r, ch) = *reinterpret_cast<const uint4*>(p.res + to_row * p.N + col);
+                            *patch_at(r, ch) = *reinterpret_cast<const uint4*>(p.res + to_row * p.N + col);
                         });
                         __syncwarp();
                     }
@@ -549,15 +659,15 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                                 Vec<float>::store(to + p.N + 4, g + 4);
                             }
                         } else {
-                            if constexpr (EPI == EPI_GLU) glu8(p, row, col, f, g);
-                            if constexpr (EPI == EPI_DGLU) dglu8(p, rg[odd][h], ru[odd][h], f, g);
+                            if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, col, f, g);
+                            if constexpr (EPI == EPI_DGLU) dglu8<GELU>(rg[odd][h], ru[odd][h], f, g);
                             if constexpr (EPI == EPI_OUT) {
                                 if (p.res)
-                                    add8(f, STAGED ? *patch_at(0, lane, ch) : *reinterpret_cast<const uint4*>(p.res + row * p.N + col));
+                                    add8(f, STAGED ? *patch_at(lane, ch) : *reinterpret_cast<const uint4*>(p.res + row * p.N + col));
                             }
-                            *(STAGED ? patch_at(0, lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + col)) = pack8(f);
+                            *(STAGED ? patch_at(lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + col)) = pack8(f);
                             if constexpr (EPI == EPI_DGLU)
-                                *(STAGED ? patch_at(1, lane, ch) : reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + col)) = pack8(g);
+                                *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + col) = pack8(g);
                         }
                     }
                     if constexpr (EPI == EPI_DGLU) fetch(chunk(k + 2), rg[odd], ru[odd]);
@@ -565,8 +675,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (STAGED && k % 4 == 3) {
                         each_line(b0, [&](int r, int ch, int64_t to_row, int col) {
                             __nv_bfloat16* to = p.out + to_row * p.ldo + col;
-                            *reinterpret_cast<uint4*>(to) = *patch_at(0, r, ch);
-                            if (EPI == EPI_DGLU) *reinterpret_cast<uint4*>(to + p.N) = *patch_at(1, r, ch);
+                            *reinterpret_cast<uint4*>(to) = *patch_at(r, ch);
                         });
                         __syncwarp();
                     }
@@ -579,6 +688,9 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 else mbar_arrive(&sb->tempty[acc]);
             }
         }
+        // an aborted warp leaves no copy in flight
+        for (; BULK && in_used < in_sent; ++in_used)
+            mbar_wait_timed(&sb->in[warp - EPI_WARP0][in_used & 1], (uint32_t)(in_used >> 1) & 1u);
     }
 
     __syncthreads();
@@ -622,7 +734,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 }
 
 // The partial sums of a split contraction in split order, then the epilogue.
-template <int EPI>
+template <int EPI, bool GELU>
 __global__ void ffn_join_kernel(const FfnParams p) {
     const int vec = p.N / 8;
     const int64_t total = (int64_t)p.M * vec;
@@ -644,12 +756,12 @@ __global__ void ffn_join_kernel(const FfnParams p) {
             add(f, from);
             if (EPI == EPI_GLU) add(g, from + p.N);
         }
-        if constexpr (EPI == EPI_GLU) glu8(p, row, c, f, g);
+        if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
         if constexpr (EPI == EPI_DGLU) {
             Raw24 rg, ru;
             rg.load(p, at24(p, row, c));
             ru.load(p, at24(p, row, p.N + c));
-            dglu8(p, rg, ru, f, g);
+            dglu8<GELU>(rg, ru, f, g);
             *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
         }
         if constexpr (EPI == EPI_OUT) {
@@ -693,7 +805,7 @@ struct Plan {
 //             and its bytes into one SM
 //   all       the weights from HBM
 //   a split   the partial sums written and read back, and the join's launch
-Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
+Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu, bool amn, bool bmn) {
     Plan best{};
     double best_cost = 1e30;
     const bool pair = M > BM;
@@ -702,13 +814,14 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool amn, 
     const int step = bmn ? (pair ? 128 : 64) : (pair ? 32 : 16);
     const int a_rows = !pair && !amn ? (int)(M + 7) / 8 * 8 : BM;
     const int64_t m_units = pair ? (M + 2 * BM - 1) / (2 * BM) : 1;
+    const int keep = pair ? (dglu ? IN_AREA : STAGING) : 0;      // the epilogue's end of the area
     for (int bn = MAX_BN; bn >= (bmn ? step : 64); bn -= step) {
         const int width = glu ? bn / 2 : bn;
         const int64_t n_tiles = (N + width - 1) / width;
         const int64_t tiles = m_units * n_tiles;
         const int a_bytes = a_rows * ROWB, b_bytes = (pair ? bn / 2 : bn) * ROWB;
         // the MMA reads 128 rows of A whatever was staged: the last stage's lie inside the ring too
-        const int stages = std::min(MAX_STAGES, (TILE_AREA - (pair ? STAGING : 0) - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
+        const int stages = std::min(MAX_STAGES, (TILE_AREA - keep - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
         const double stage = std::max(std::max(0.365 * bn / 256, 1.4 / stages), (a_bytes + b_bytes) / 80e3);
         for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
             if (splits > 1 && tiles * (splits - 1) >= workers) break;
@@ -727,7 +840,7 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool amn, 
 
 // The search takes about a microsecond and a call needs each of its plans
 // three times: the last ones of this thread are kept, by their sizes.
-Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool amn, bool bmn) {
+Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool dglu, bool amn, bool bmn) {
     struct Entry {
         int64_t M = -1, N = 0;
         int kb = 0, num_sms = 0, kind = 0;
@@ -736,12 +849,12 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     constexpr int kEntries = 16;
     static thread_local Entry cache[kEntries];
     static thread_local int next = 0;
-    const int kind = glu | amn << 1 | bmn << 2;
+    const int kind = glu | amn << 1 | bmn << 2 | dglu << 3;
     for (const Entry& e : cache)
         if (e.M == M && e.N == N && e.kb == kb && e.num_sms == c->num_sms && e.kind == kind) return e.plan;
     Entry& e = cache[next];
     next = (next + 1) % kEntries;
-    e.plan = search_plan(c->num_sms, M, N, kb, glu, amn, bmn);
+    e.plan = search_plan(c->num_sms, M, N, kb, glu, dglu, amn, bmn);
     e.M = M;
     e.N = N;
     e.kb = kb;
@@ -750,10 +863,10 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     return e.plan;
 }
 
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU>
 cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, bool pdl,
                        cudaStream_t s) {
-    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8>;
+    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU>;
     static std::mutex mu;
     static int max_units[64] = {};              // CTAs or pairs resident at once, per device
     int dev = 0;
@@ -811,7 +924,7 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
                     FfnParams p, float* part, const char* name, bool after, cudaStream_t s) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int kstep = F8 ? 128 : 64;
-    const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, AMN, BMN);
+    const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, EPI == EPI_DGLU, AMN, BMN);
     const bool pdl = after && !c->prof;
     p.M = (int)M;
     p.N = (int)N;
@@ -837,12 +950,17 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     if (!ok) return cudaErrorInvalidValue;
     prof_begin(c, s, name);
     cudaError_t e;
-    if (pl.splits == 1)
-        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, pdl, s)
-                    : launch_one<EPI, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, pdl, s);
+    constexpr bool ACT = EPI == EPI_GLU || EPI == EPI_DGLU;
+    const bool gelu = ACT && p.act == ENGRAM_ACT_GELU;
+    if (pl.splits > 1)
+        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
+                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
+    else if (gelu)
+        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT>(ma, mb, p, c->num_sms, pdl, s)
+                    : launch_one<EPI, GLU, AMN, BMN, false, F8, ACT>(ma, mb, p, c->num_sms, pdl, s);
     else
-        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8>(ma, mb, p, c->num_sms, pdl, s)
-                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8>(ma, mb, p, c->num_sms, pdl, s);
+        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
+                    : launch_one<EPI, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
     prof_end(c, s);
     if (e == cudaSuccess && pl.splits > 1) {
         prof_begin(c, s, "ffn_join");
@@ -857,7 +975,7 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = c->prof ? 0 : 1;
-        e = cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI>, p);
+        e = gelu ? cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI, ACT>, p) : cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI, false>, p);
         prof_end(c, s);
     }
     return e;
@@ -893,14 +1011,14 @@ FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad
     auto kb = [](int64_t K) { return (int)((K + 63) / 64); };
     size_t part = 0;
     if (grad) {
-        part = std::max(part, make_plan(c, n, f, kb(d), false, false, true).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, false, true).part_bytes);
-        part = std::max(part, make_plan(c, d, f, kb(n), false, true, true).part_bytes);
-        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, true, true).part_bytes);
+        part = std::max(part, make_plan(c, n, f, kb(d), false, true, false, true).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, false, false, true).part_bytes);
+        part = std::max(part, make_plan(c, d, f, kb(n), false, false, true, true).part_bytes);
+        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, false, true, true).part_bytes);
     } else {
         const bool f8 = c->cfg.dtype == ENGRAM_FP8;
-        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false, false).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(f), false, false, false).part_bytes);
+        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false, false, false).part_bytes);
+        part = std::max(part, make_plan(c, n, d, kb(f), false, false, false, false).part_bytes);
     }
     FfnWs w{};
     char* p = static_cast<char*>(base);
