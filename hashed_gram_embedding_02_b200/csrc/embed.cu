@@ -151,8 +151,9 @@ constexpr int kSortTile = kSortThreads * kSortIpt;
 constexpr int kMaxSortCtas = 256;
 constexpr int kSmallThreads = 512;
 constexpr int kSmallWarps = kSmallThreads / 32;
-constexpr int kSmallIpt = 4;
-constexpr int kSortSmall = kSmallThreads * kSmallIpt;      // 2048
+constexpr int kSmallIpt = 16;                              // at most, elements per thread
+constexpr int kSortSmall = kSmallThreads * kSmallIpt;      // 8192
+constexpr size_t small_smem(int ipt) { return (size_t)kSmallThreads * ipt * 6 + kSmallWarps * kDigits * 2; }
 constexpr int64_t kMaxEmbedRows = (int64_t)1 << 24;
 // Gradients of at most this many bytes are cleared whole: clearing 64 MB takes
 // 9 us, the bitmap and a launch of their own cost as much (256 rows, V 4096, d
@@ -292,7 +293,8 @@ embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restri
     }
 }
 
-// At most kSortSmall positions: all passes in one CTA's shared memory.
+// At most kSmallThreads * IPT positions: all passes in one CTA's shared memory.
+template <int IPT>
 __global__ void __launch_bounds__(kSmallThreads)
 embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__ keys_out,
                         uint32_t* __restrict__ pos_out, uint32_t* touched, int64_t touched_words, uint32_t* count,
@@ -301,17 +303,17 @@ embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__
         zero.run(blockIdx.x - 1, gridDim.x - 1);
         return;
     }
-    __shared__ uint32_t s_key[kSortSmall];
-    __shared__ uint16_t s_pos[kSortSmall];
-    __shared__ uint16_t s_cnt[kSmallWarps][kDigits];
+    extern __shared__ uint32_t s_key[];
+    uint16_t* const s_pos = reinterpret_cast<uint16_t*>(s_key + kSmallThreads * IPT);
+    uint16_t(*const s_cnt)[kDigits] = reinterpret_cast<uint16_t(*)[kDigits]>(s_pos + kSmallThreads * IPT);
     __shared__ uint32_t s_scan[kSmallWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int64_t k = tid; k < touched_words; k += kSmallThreads) touched[k] = 0;
     if (tid == 0) *count = 0;
-    uint32_t key[kSmallIpt], ps[kSmallIpt], rank[kSmallIpt];
-    const int w0 = warp * (32 * kSmallIpt);
+    uint32_t key[IPT], ps[IPT], rank[IPT];
+    const int w0 = warp * (32 * IPT);
 #pragma unroll
-    for (int k = 0; k < kSmallIpt; ++k) {
+    for (int k = 0; k < IPT; ++k) {
         const int i = w0 + k * 32 + lane;
         key[k] = i < n ? sort_key(src, i, status) : 0u;
         ps[k] = (uint32_t)i;
@@ -322,7 +324,7 @@ embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__
         for (int k = tid; k < kSmallWarps * kDigits; k += kSmallThreads) (&s_cnt[0][0])[k] = 0;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSmallIpt; ++k) {
+        for (int k = 0; k < IPT; ++k) {
             const bool live = w0 + k * 32 + lane < n;
             const uint32_t digit = (key[k] >> shift) & (kDigits - 1);
             const uint32_t mask = __match_any_sync(0xffffffffu, live ? digit : 0xffffffffu);
@@ -354,7 +356,7 @@ embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSmallIpt; ++k) {
+        for (int k = 0; k < IPT; ++k) {
             if (w0 + k * 32 + lane < n) {
                 const uint32_t to = s_cnt[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k];
                 s_key[to] = key[k];
@@ -363,7 +365,7 @@ embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSmallIpt; ++k) {
+        for (int k = 0; k < IPT; ++k) {
             const int i = w0 + k * 32 + lane;
             if (i < n) {
                 key[k] = s_key[i];
@@ -373,7 +375,7 @@ embed_sort_small_kernel(TokSource src, int n, int passes, uint32_t* __restrict__
     }
     // the bitmap was cleared above by this CTA alone; the barriers of the passes order the two
 #pragma unroll
-    for (int k = 0; k < kSmallIpt; ++k) {
+    for (int k = 0; k < IPT; ++k) {
         const int i = w0 + k * 32 + lane;
         if (i < n) {
             keys_out[i] = key[k];
@@ -529,22 +531,23 @@ __global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh) {
     }
 }
 
-// The cut runs: a CTA takes 512 columns of one run; its two halves sum the
-// first and the second half of the run's parts, which are then added.
-constexpr int kJoinHalf = 128;
-constexpr int kJoinCols = kJoinHalf * 4;
+// The cut runs: a CTA takes 4 * `lanes` columns of one run; its 256 / lanes
+// groups of threads sum consecutive shares of the run's parts, which are then
+// added in order.  Narrow rows leave more groups (a token that takes 38 % of
+// 6732 positions, d 96: 39 us with two groups, 13 us with eight).
+constexpr int kJoinThreads = 256;
 
 template <int PIECE, bool ACC>
-__global__ void __launch_bounds__(2 * kJoinHalf) embed_join_kernel(EmbedGrad p) {
-    __shared__ float4 s_sum[kJoinHalf];
-    const int t = threadIdx.x & (kJoinHalf - 1), half = threadIdx.x / kJoinHalf;
-    const int slices = (p.d + kJoinCols - 1) / kJoinCols;
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGrad p, int lanes) {
+    __shared__ float4 s_sum[kJoinThreads];
+    const int t = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kJoinThreads / lanes;
+    const int slices = (p.d + 4 * lanes - 1) / (4 * lanes);
     const int64_t work = (int64_t)*p.count * slices;
     for (int64_t u = blockIdx.x; u < work; u += gridDim.x) {
         const uint4 run = p.cut[u / slices];
         const int64_t p0 = run.x, m = run.y;               // parts: p0's last run, then the first runs of m - 1 pieces
-        const int col = (int)(u % slices) * kJoinCols + t * 4;
-        const int64_t a = half ? (m + 1) / 2 : 0, b = half ? m : (m + 1) / 2;
+        const int col = ((int)(u % slices) * lanes + t) * 4;
+        const int64_t per = (m + groups - 1) / groups, a = group * per, b = min(m, a + per);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < p.d) {
 #pragma unroll 8
@@ -556,11 +559,17 @@ __global__ void __launch_bounds__(2 * kJoinHalf) embed_join_kernel(EmbedGrad p) 
                 acc.w += x.w;
             }
         }
-        if (half) s_sum[t] = acc;
+        s_sum[threadIdx.x] = acc;
         __syncthreads();
-        if (!half && col < p.d) {
-            const float4 x = s_sum[t];
-            const float f[4] = {acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w};
+        if (group == 0 && col < p.d) {
+            for (int g = 1; g < groups && g * per < m; ++g) {
+                const float4 x = s_sum[g * lanes + t];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+            const float f[4] = {acc.x, acc.y, acc.z, acc.w};
             put_row<4>(p.d_E + (int64_t)run.z * p.d + col, f, p.scale, ACC, false);
         }
         __syncthreads();
@@ -650,9 +659,11 @@ cudaError_t reduce_and_join(engram_ctx* c, const EmbedGrad& p, const void* dh, c
     prof_end(c, s);
     if (e != cudaSuccess || p.n_pieces < 2) return e;
     prof_begin(c, s, "embed_join");
-    const int slices = (p.d + kJoinCols - 1) / kJoinCols;
+    int lanes = 1;
+    while (lanes < 64 && lanes * 4 < p.d) lanes <<= 1;
+    const int slices = (p.d + 4 * lanes - 1) / (4 * lanes);
     const unsigned blocks = (unsigned)std::min<int64_t>(p.n_pieces * slices, (int64_t)c->num_sms * 8);
-    embed_join_kernel<PIECE, ACC><<<blocks, 2 * kJoinHalf, 0, s>>>(p);
+    embed_join_kernel<PIECE, ACC><<<blocks, kJoinThreads, 0, s>>>(p, lanes);
     prof_end(c, s);
     return cudaGetLastError();
 }
@@ -737,8 +748,16 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     cudaError_t e = cudaSuccess;
     prof_begin(c, s, "embed_sort");
     if (n <= kSortSmall) {
-        embed_sort_small_kernel<<<1 + zero_ctas, kSmallThreads, 0, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched,
-                                                                        touched_words, w.count, zero, c->d_status);
+        auto go = [&](auto kern, int ipt) {
+            const size_t smem = small_smem(ipt);
+            if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess)
+                kern<<<1 + zero_ctas, kSmallThreads, smem, s>>>(src, (int)n, passes, w.keys[0], w.pos[0], touched, touched_words,
+                                                                w.count, zero, c->d_status);
+        };
+        if (n <= kSmallThreads) go(embed_sort_small_kernel<1>, 1);
+        else if (n <= 4 * kSmallThreads) go(embed_sort_small_kernel<4>, 4);
+        else go(embed_sort_small_kernel<kSmallIpt>, kSmallIpt);
     } else {
         const int64_t per = sort_part(n);
         const unsigned parts = (unsigned)((n + per - 1) / per);

