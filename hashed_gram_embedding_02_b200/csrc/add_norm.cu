@@ -17,6 +17,7 @@
 #include <cuda_fp8.h>
 
 #include "ctx.cuh"
+#include "tc.cuh"
 
 namespace engram {
 namespace {
@@ -264,11 +265,11 @@ __global__ void __launch_bounds__(kMaxTpr) add_norm_grad_kernel(const T* d_y, co
     }
 }
 
-// dg: 32 columns per CTA, eight warps over the partial rows, added in warp order
+// dg: 32 columns per CTA, its warps over the partial rows, added in warp order
 constexpr int kGainWarps = 32;
-__global__ void __launch_bounds__(kGainWarps * 32) gain_grad_kernel(const float* __restrict__ part, int rows, int d,
-                                                                    float* __restrict__ d_gain) {
+__global__ void __launch_bounds__(kGainWarps * 32) gain_grad_kernel(const float* part, int rows, int d, float* d_gain) {
     __shared__ float s_sum[kGainWarps][32];
+    grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float acc = 0.f;
@@ -408,9 +409,9 @@ engram_status engram_add_norm_grad(engram_ctx* c, const void* d_y, const void* d
     prof_end(c, s);
     if (e == cudaSuccess && d_gain) {
         prof_begin(c, s, "gain_grad");
-        gain_grad_kernel<<<(d + 31) / 32, kGainWarps * 32, 0, s>>>(part, (int)(grad_ctas(c, n, g) * g.rb), d, d_gain);
+        e = launch_after(c, gain_grad_kernel, (unsigned)((d + 31) / 32), dim3(kGainWarps * 32), 0, s, part,
+                         (int)(grad_ctas(c, n, g) * g.rb), d, d_gain);
         prof_end(c, s);
-        e = cudaGetLastError();
     }
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("residual norm gradient launches", e);
 }

@@ -56,6 +56,24 @@ void prof_reset(engram_ctx* c);
 void prof_begin(engram_ctx* c, cudaStream_t s, const char* name);
 void prof_end(engram_ctx* c, cudaStream_t s);
 
+// A launch that waits on the device for the one before it on the stream (timed
+// calls put events in between and launch plainly).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(const engram_ctx* c, void (*kern)(KArgs...), unsigned grid, dim3 block, size_t smem, cudaStream_t s,
+                         Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = c->prof ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, KArgs(args)...);
+}
+
 engram_status check_device(const engram_ctx* c);
 
 // Scratch of one forward over B sequences of L computed rows:

@@ -23,10 +23,13 @@
 //   3. join: the parts of each cut run, in order.
 // Between 1 and 2 the rows of the tokens that do not occur are cleared (a small
 // dE is cleared whole by the sort's first launch).
-// The order of every sum depends on the tokens alone.
+// The order of every sum depends on the tokens alone.  The launches behind the
+// first are programmatic dependents of one another: each waits at its start
+// for the one before, which hides most of its launch.
 #include <algorithm>
 
 #include "ctx.cuh"
+#include "tc.cuh"
 
 namespace engram {
 namespace {
@@ -219,18 +222,19 @@ __global__ void embed_keys_kernel(TokSource src, int64_t n, int64_t per, uint32_
 // One pass: stable scatter by the digit at `shift`.  hist_next (nullable,
 // cleared before): counts of the next digit per part of the output.
 __global__ void __launch_bounds__(kSortThreads)
-embed_scatter_kernel(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, int64_t per,
-                     int shift, const uint32_t* __restrict__ hist, uint32_t* __restrict__ keys_out,
-                     uint32_t* __restrict__ pos_out, uint32_t* hist_next) {
+embed_scatter_kernel(const uint32_t* keys, const uint32_t* pos, int64_t n, int64_t per, int shift, const uint32_t* hist,
+                     uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint32_t* hist_next) {
     __shared__ uint32_t s_base[kDigits];                   // where this part's next element of a digit goes
     __shared__ uint32_t s_cnt[kSortWarps][kDigits];
     __shared__ uint32_t s_scan[kSortWarps];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int parts = gridDim.x, me = blockIdx.x;
     // two digits per thread: totals, and the counts of the parts before this one
     uint32_t tot[2] = {0, 0}, mine[2] = {0, 0};
     for (int p = 0; p < parts; ++p) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(hist + (int64_t)p * kDigits) + tid);
+        const uint2 v = *(reinterpret_cast<const uint2*>(hist + (int64_t)p * kDigits) + tid);
         tot[0] += v.x;
         tot[1] += v.y;
         if (p < me) {
@@ -443,10 +447,12 @@ __device__ __forceinline__ void put_row(float* to, const float* f, float scale, 
 // side stream starves the sums: 316 and 292 us for a call, so 276 us).
 constexpr int kFillThreads = 512;
 
-__global__ void __launch_bounds__(kFillThreads) embed_fill_kernel(const uint32_t* __restrict__ touched, uint32_t V, int d,
+__global__ void __launch_bounds__(kFillThreads) embed_fill_kernel(const uint32_t* touched, uint32_t V, int d,
                                                                   float* __restrict__ d_E) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t w = blockIdx.x, bits = __ldg(touched + w);
+    const uint32_t w = blockIdx.x, bits = touched[w];
     for (uint32_t r = warp; r < 32 && w * 32 + r < V; r += kFillThreads / 32) {
         if ((bits >> r) & 1u) continue;
         float4* row = reinterpret_cast<float4*>(d_E + (int64_t)(w * 32 + r) * d);
@@ -458,6 +464,8 @@ template <typename T, int PIECE, bool ACC>
 __global__ void embed_reduce_kernel(EmbedGrad p, const T* __restrict__ dh) {
     constexpr int EPC = Vec<T>::N;
     extern __shared__ uint32_t s_mem[];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     const int cpr = p.d / EPC;
     const int64_t piece = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     // keys of the piece with one neighbour on each side (kNone outside the list), and its positions
@@ -540,6 +548,8 @@ constexpr int kJoinThreads = 256;
 template <int PIECE, bool ACC>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGrad p, int lanes) {
     __shared__ float4 s_sum[kJoinThreads];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
     const int t = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kJoinThreads / lanes;
     const int slices = (p.d + 4 * lanes - 1) / (4 * lanes);
     const int64_t work = (int64_t)*p.count * slices;
@@ -647,8 +657,7 @@ cudaError_t launch_reduce(const engram_ctx* c, const EmbedGrad& p, const void* d
     const dim3 block(g.tpr, g.rb);
     const unsigned pieces = (unsigned)((p.n_pieces + g.rb - 1) / g.rb);
     const size_t smem = (size_t)g.rb * (2 * PIECE + 2) * 4;
-    embed_reduce_kernel<T, PIECE, ACC><<<pieces, block, smem, s>>>(p, static_cast<const T*>(dh));
-    return cudaGetLastError();
+    return launch_after(c, embed_reduce_kernel<T, PIECE, ACC>, pieces, block, smem, s, p, static_cast<const T*>(dh));
 }
 
 template <int PIECE, bool ACC>
@@ -663,9 +672,9 @@ cudaError_t reduce_and_join(engram_ctx* c, const EmbedGrad& p, const void* dh, c
     while (lanes < 64 && lanes * 4 < p.d) lanes <<= 1;
     const int slices = (p.d + 4 * lanes - 1) / (4 * lanes);
     const unsigned blocks = (unsigned)std::min<int64_t>(p.n_pieces * slices, (int64_t)c->num_sms * 8);
-    embed_join_kernel<PIECE, ACC><<<blocks, kJoinThreads, 0, s>>>(p, lanes);
+    e = launch_after(c, embed_join_kernel<PIECE, ACC>, blocks, dim3(kJoinThreads), 0, s, p, lanes);
     prof_end(c, s);
-    return cudaGetLastError();
+    return e;
 }
 
 engram_status check_tokens(const engram_ctx* c, int32_t B, int32_t T, int64_t tok_stride, int32_t t_begin,
@@ -770,8 +779,18 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
             // the counts of pass p + 1 go where those of pass p - 1 were
             if (p > 0 && !last) e = cudaMemsetAsync(w.hist[at ^ 1], 0, (size_t)w.hist_words * 4, s);
             if (e != cudaSuccess) break;
-            embed_scatter_kernel<<<parts, kSortThreads, 0, s>>>(w.keys[at], w.pos[at], n, per, p * kDigitBits, w.hist[at],
-                                                                w.keys[at ^ 1], w.pos[at ^ 1], last ? nullptr : w.hist[at ^ 1]);
+            // the third pass on follows a clear, not a kernel
+            auto args = [&](auto&& go) {
+                return go(w.keys[at], w.pos[at], n, per, p * kDigitBits, w.hist[at], w.keys[at ^ 1], w.pos[at ^ 1],
+                          last ? nullptr : w.hist[at ^ 1]);
+            };
+            const bool plain = p > 0 && !last;
+            e = args([&](auto... a) {
+                if (!plain) return launch_after(c, embed_scatter_kernel, parts, dim3(kSortThreads), 0, s, a...);
+                embed_scatter_kernel<<<parts, kSortThreads, 0, s>>>(a...);
+                return cudaGetLastError();
+            });
+            if (e != cudaSuccess) break;
             at ^= 1;
         }
     }
@@ -779,7 +798,7 @@ engram_status engram_embed_grad(engram_ctx* c, const int32_t* tok, int32_t B, in
     if (rest && e == cudaSuccess) {
         prof_begin(c, s, "embed_fill");
         const unsigned blocks = (unsigned)((V + 31) / 32);
-        embed_fill_kernel<<<blocks, kFillThreads, 0, s>>>(w.touched, (uint32_t)V, d, d_E);
+        e = launch_after(c, embed_fill_kernel, blocks, dim3(kFillThreads), 0, s, w.touched, (uint32_t)V, d, d_E);
         prof_end(c, s);
     }
     if (e == cudaSuccess) e = cudaGetLastError();

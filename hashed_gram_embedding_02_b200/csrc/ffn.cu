@@ -976,16 +976,8 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
         prof_begin(c, s, "ffn_join");
         const int64_t threads = M * (N / 8);
         const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(blocks, 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = c->prof ? 0 : 1;
-        e = gelu ? cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI, ACT>, p) : cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI, false>, p);
+        e = gelu ? launch_after(c, ffn_join_kernel<EPI, ACT>, blocks, dim3(256), 0, s, p)
+                 : launch_after(c, ffn_join_kernel<EPI, false>, blocks, dim3(256), 0, s, p);
         prof_end(c, s);
     }
     return e;
