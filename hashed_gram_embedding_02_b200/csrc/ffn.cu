@@ -100,6 +100,7 @@ struct FfnParams {
     const float* col_scale;     // FP8: [2N]
     float* part;                // PART: [splits][M][N] (GLU: [splits][M][2N])
     uint32_t* status;
+    int late_wait;              // nothing here depends on the kernel before: wait for it only before leaving
     int stall;                  // test hook: CTA 0 announces its first B stage but never loads it
 };
 
@@ -373,7 +374,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             int* issued = &sb->issued[warp];
             // A may come from a kernel of this call that is still running; B
             // (weights, x, the saved a) never does
-            if (is_a) grid_dep_wait();
+            if (is_a && !p.late_wait) grid_dep_wait();
             int it = 0, s = 0;
             uint32_t ph = 0;
             for (int u = unit0; u < num_units && !sb->abort_flag; u += step) {
@@ -483,7 +484,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         // the warp's k-th chunk of 16 columns
         auto chunk = [&](int k) { return part * BLK + k / (BLK / 16) * (BLK * EPI_PARTS) + k % (BLK / 16) * 16; };
         int tc = 0;
-        grid_dep_wait();        // reads what earlier kernels wrote, writes what they may still read
+        if (!p.late_wait) grid_dep_wait();   // reads what earlier kernels wrote, writes what they may still read
         // BULK: 32 columns of g and u at a time, copied by the warp's lane 0 a
         // block ahead, over tiles too.  Loads into registers keep too few
         // bytes in flight: the epilogue of 16384 rows, f 6912 alone took 399
@@ -703,6 +704,8 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             mbar_wait_timed(&sb->in[warp - EPI_WARP0][in_used & 1], (uint32_t)(in_used >> 1) & 1u);
     }
 
+    // this grid must not complete before the one it depends on: those behind it count on both
+    if (p.late_wait) grid_dep_wait();
     __syncthreads();
     bool aborted = sb->abort_flag != 0;
     if constexpr (PAIR) {
@@ -929,9 +932,11 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
 // may be its programmatic dependent (timed calls put events in between).
 // One product: A [M][K] (or [K][M] with AMN), B [N][K] (or [K][N] with BMN;
 // GLU: [2N][K]), and its epilogue, through partial sums when the plan splits.
+// independent: it reads and writes nothing of the kernels before it in this
+// call (it may run beside them, unless it needs the shared partial sums).
 template <int EPI, bool AMN, bool BMN, bool F8 = false>
 cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                    FfnParams p, float* part, const char* name, bool after, cudaStream_t s) {
+                    FfnParams p, float* part, const char* name, bool after, cudaStream_t s, bool independent = false) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int kstep = F8 ? 128 : 64;
     const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, EPI == EPI_DGLU, AMN, BMN);
@@ -947,6 +952,7 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     p.b_bytes = pl.b_bytes;
     p.stages = pl.stages;
     p.raster = 8;
+    p.late_wait = independent && pdl && pl.splits == 1;
     p.status = c->d_status;
     p.part = part;
     p.b_rows = GLU || pl.pair ? pl.bn / 2 : pl.bn;
@@ -1163,7 +1169,13 @@ engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, con
     p.gu_hi = sv.hi;
     p.gu_lo = sv.lo;
     cudaError_t e = product<EPI_DGLU, false, true>(c, d_y, d, Wd, f, n, f, d, p, w.part, "ffn_d_gate_up", false, s);
+    // d_Wd needs neither dg nor du: its tiles fill the SMs that d_gate_up leaves
     FfnParams o{};
+    if (e == cudaSuccess) {
+        o.out = static_cast<__nv_bfloat16*>(d_Wd);
+        o.ldo = f;
+        e = product<EPI_OUT, true, true>(c, d_y, d, sv.a, pitch(f), d, f, n, o, w.part, "ffn_d_Wd", true, s, true);
+    }
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_x);
         o.ldo = d;
@@ -1172,11 +1184,6 @@ engram_status engram_ffn_grad(engram_ctx* c, const void* d_y, const void* x, con
     if (e == cudaSuccess) {
         o.out = static_cast<__nv_bfloat16*>(d_Wgu);
         e = product<EPI_OUT, true, true>(c, w.mid, p.ldo, x, d, 2 * (int64_t)f, d, n, o, w.part, "ffn_d_Wgu", true, s);
-    }
-    if (e == cudaSuccess) {
-        o.out = static_cast<__nv_bfloat16*>(d_Wd);
-        o.ldo = f;
-        e = product<EPI_OUT, true, true>(c, d_y, d, sv.a, pitch(f), d, f, n, o, w.part, "ffn_d_Wd", true, s);
     }
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail("feed-forward backward launches", e);
 }
