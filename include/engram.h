@@ -537,7 +537,8 @@ ENGRAM_API engram_status engram_add_norm_grad(engram_ctx* ctx, const void* d_y, 
  *   d_Wd [d][f] = d_y^T (act(g) * u),
  * all bf16, each sum in fp32 and rounded once when stored (dg and du are held
  * in bf16 between the products, act(g) * u is the saved one); d_Wgu and d_Wd are
- * overwritten.  d_x must not overlap the inputs.  ENGRAM_BF16 contexts only.
+ * overwritten.  The outputs must not overlap the inputs.  ENGRAM_BF16 contexts
+ * only.
  * Scratch: engram_ffn_grad_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
  *
  * The workspace sizes are 0 for arguments the call refuses.  Results are the

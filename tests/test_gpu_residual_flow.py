@@ -153,6 +153,38 @@ def test_captured_steps_replay_the_eager_bits(eb):
     del graphs, outs
 
 
+@pytest.mark.parametrize("T", [500, 3000, 20011])         # the sorts of one CTA, narrow and wide, and of several
+def test_captured_embedding_gradient(eb, T):
+    eng = engine(eb, 264, 70001)                          # 74 MB: the untouched rows are cleared apart
+    small = engine(eb, 264, 5000)                         # cleared whole
+    for e, V in ((eng, 70001), (small, 5000)):
+        tok, d_h = tokens(1, 2, T, V), randn(2, 2 * T, 264)
+        out = torch.full((V, 264), 3.0, device="cuda")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        e.embed_grad(tok, d_h, out=out, stream=side)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            e.embed_grad(tok, d_h, out=out)
+        for k, kind in enumerate(("half", "one", "distinct")):
+            tok.copy_(tokens(k + 5, 2, T, V, kind))
+            out.fill_(float("nan"))
+            g.replay()
+            assert torch.equal(out, e.embed_grad(tok, d_h)), kind
+
+
+def test_embed_grad_into_rows_of_16_byte_alignment(eb):
+    eng = engine(eb, 72, 500)
+    tok, d_h = tokens(1, 3, 700, 500), randn(2, 2100, 72)
+    want = eng.embed_grad(tok, d_h)
+    flat = torch.full((500 * 72 + 8,), 9.0, device="cuda")
+    out = flat[4:-4].view(500, 72)
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(eng.embed_grad(tok, d_h, out=out), want)
+    assert (flat[:4] == 9).all() and (flat[-4:] == 9).all()
+
+
 def test_norm_codes_feed_the_fp8_block(eb):
     """the 8-bit path: embed, norm with E4M3 output, feed-forward block on the codes, residual"""
     d, f, n = 256, 392, 77
