@@ -8,6 +8,7 @@ plus its workspace.  PyTorch is used only for device memory and streams.
 
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 from .binding import (  # noqa: F401  (re-exported C ABI names)
@@ -207,7 +208,7 @@ class Engram:
 
     # ---- the residual stream around the module
 
-    @property
+    @functools.cached_property
     def dtype(self):
         """torch dtype of the hidden states (h, Y)"""
         import torch
@@ -228,8 +229,8 @@ class Engram:
     def _want_tokens(self, tok, t_begin: int):
         """(B, T, row stride) of a token tensor whose rows may be wider than T."""
         import torch
-        if tok.dim() != 2:
-            raise ValueError(f"tok has {tok.dim()} dimensions, needs 2")
+        if tok.ndim != 2:
+            raise ValueError(f"tok has {tok.ndim} dimensions, needs 2")
         if tok.dtype is not torch.int32 or tok.device != self.device:
             raise ValueError(f"tok is {tok.dtype} on {tok.device}, needs torch.int32 on {self.device}")
         B, T = tok.shape
