@@ -839,7 +839,8 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
         for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
             if (splits > 1 && tiles * (splits - 1) >= workers) break;
             const int64_t waves = (tiles * splits + workers - 1) / workers;
-            double cost = std::max(waves * ((kb + splits - 1) / splits) * stage, (double)kb * ROWB * cols / 6.4e6);
+            const double units = waves * ((kb + splits - 1) / splits) * stage, hbm = (double)kb * ROWB * cols / 6.4e6;
+            double cost = std::max(units, hbm) + 0.2 * std::min(units, hbm);     // they overlap, but not wholly
             if (splits > 1) cost += 3.0 + (double)splits * M * cols * 8 / 6e6;
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
