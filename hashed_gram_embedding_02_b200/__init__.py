@@ -206,7 +206,9 @@ class Engram:
         """shard_table[row - first] -= lr * grad for the listed global rows."""
         engram_shard_sgd(self.ctx, n_shards, shard, rows, grad, n_unique, rows.shape[0], shard_table, lr, stream)
 
-    # ---- the residual stream around the module
+    # ---- the residual stream around the module.  With a stream given, the work
+    # and the tensors made here belong to it: a caller that uses them on
+    # another stream orders the two (wait_stream, record_stream).
 
     @functools.cached_property
     def dtype(self):
