@@ -98,7 +98,8 @@ struct FfnParams {
     const __nv_bfloat16* res;   // OUT: [M][N] or null
     const float* row_scale;     // FP8: [M]
     const float* col_scale;     // FP8: [2N]
-    float* part;                // PART: [splits][M][N] (GLU: [splits][M][2N])
+    float4* part;               // PART: [splits] of a matrix [M][N] (GLU: [M][2N]): see part_at
+    int part_rows;              // log2 of its block's rows
     uint32_t* status;
     int late_wait;              // nothing here depends on the kernel before: wait for it only before leaving
     int stall;                  // test hook: CTA 0 announces its first B stage but never loads it
@@ -272,6 +273,30 @@ __device__ __forceinline__ void add8(float* v, const uint4& r) {
 
 __device__ __forceinline__ uint4 pack8(const float* f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// Partial sums lie four columns an element, [row / R][column / 4][row % R]; R is
+// 32 where there are more rows: a warp's rows are contiguous where they are
+// written and read (d 2560, f 10240: 128 rows 44.9 us with R = 1, 41.5 with 32;
+// 256 rows 62 and 55; n 615, d 496, f 4952 with its backward 92 and 87).  Up to
+// 32 rows R is 1: blocks cost more than they give where rows are few (one row
+// 35.7 and 38; 7 rows, d 2048, f 8192, 29.5 and 31.8).
+constexpr int PART_ROWS_LOG2 = 5;
+__device__ __forceinline__ int64_t part_at(int cols, int64_t row, int col, int rows_log2) {
+    return (((row >> rows_log2) * (cols / 4) + col / 4) << rows_log2) + (row & ((1 << rows_log2) - 1));
+}
+__host__ __device__ inline int64_t part_size(int64_t rows, int cols, int rows_log2) {
+    return ((rows + (1 << rows_log2) - 1) >> rows_log2 << rows_log2) * (cols / 4);
+}
+
+// sums of eight columns over n matrices `next` elements apart
+__device__ __forceinline__ void add_parts(float* acc, const float4* at, int n, int64_t next, int rows_log2) {
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const float4 a = at[k * next], b = at[k * next + (1 << rows_log2)];
+        acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+        acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+    }
 }
 
 // ---------------------------------------------------------------- kernel
@@ -661,13 +686,14 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         }
                         const int ch = (c - b0) / 8 + h;
                         if constexpr (EPI == EPI_PART) {
-                            const int64_t ld = GLU ? 2 * (int64_t)p.N : p.N;
-                            float* to = p.part + ((int64_t)w.split * p.M + row) * ld + col;
-                            Vec<float>::store(to, f);
-                            Vec<float>::store(to + 4, f + 4);
+                            const int ld = GLU ? 2 * p.N : p.N, R = 1 << p.part_rows;
+                            float4* to = p.part + w.split * part_size(p.M, ld, p.part_rows) + part_at(ld, row, col, p.part_rows);
+                            to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            to[R] = make_float4(f[4], f[5], f[6], f[7]);
                             if (GLU) {
-                                Vec<float>::store(to + p.N, g);
-                                Vec<float>::store(to + p.N + 4, g + 4);
+                                to += (int64_t)(p.N / 4) * R;
+                                to[0] = make_float4(g[0], g[1], g[2], g[3]);
+                                to[R] = make_float4(g[4], g[5], g[6], g[7]);
                             }
                         } else {
                             if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, col, f, g);
@@ -746,41 +772,42 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     }
 }
 
-// The partial sums of a split contraction in split order, then the epilogue.
+// The epilogue of eight columns whose sums are complete.
 template <int EPI, bool GELU>
+__device__ __forceinline__ void finish8(const FfnParams& p, int64_t row, int c, float* f, float* g) {
+    if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
+    if constexpr (EPI == EPI_DGLU) {
+        Raw24 rg, ru;
+        rg.load(p, at24(p, row, c));
+        ru.load(p, at24(p, row, p.N + c));
+        dglu8<GELU>(rg, ru, f, g);
+        *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
+    }
+    if constexpr (EPI == EPI_OUT) {
+        if (p.res) add8(f, *reinterpret_cast<const uint4*>(p.res + row * p.N + c));
+    }
+    *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
+}
+
+// The partial sums of a split contraction in split order, then the epilogue: a
+// thread takes eight columns of a row, its neighbours the block's other rows.
+template <int EPI, bool GELU, int ROWS_LOG2>
 __global__ void ffn_join_kernel(const FfnParams p) {
-    const int vec = p.N / 8;
-    const int64_t total = (int64_t)p.M * vec;
-    const int64_t ld = EPI == EPI_GLU ? 2 * (int64_t)p.N : p.N;
+    constexpr bool GLU = EPI == EPI_GLU;
+    constexpr int R = 1 << ROWS_LOG2;
+    const int vec = p.N / 8, ld = GLU ? 2 * p.N : p.N;
+    const int64_t next = part_size(p.M, ld, ROWS_LOG2), total = part_size(p.M, p.N, ROWS_LOG2) / 2;
     grid_dep_wait();
     grid_dep_launch_dependents();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = i / vec;
-        const int c = (int)(i - row * vec) * 8;
+        const int64_t j = i >> ROWS_LOG2, block = j / vec, row = block * R + (i & (R - 1));
+        const int c = (int)(j - block * vec) * 8;
+        if (row >= p.M) continue;
         float f[8] = {}, g[8] = {};
-        auto add = [&](float* acc, const float* from) {
-            const float4 a = *reinterpret_cast<const float4*>(from), b = *(reinterpret_cast<const float4*>(from) + 1);
-            acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-            acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
-        };
-#pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) {
-            const float* from = p.part + ((int64_t)s * p.M + row) * ld + c;
-            add(f, from);
-            if (EPI == EPI_GLU) add(g, from + p.N);
-        }
-        if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
-        if constexpr (EPI == EPI_DGLU) {
-            Raw24 rg, ru;
-            rg.load(p, at24(p, row, c));
-            ru.load(p, at24(p, row, p.N + c));
-            dglu8<GELU>(rg, ru, f, g);
-            *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
-        }
-        if constexpr (EPI == EPI_OUT) {
-            if (p.res) add8(f, *reinterpret_cast<const uint4*>(p.res + row * p.N + c));
-        }
-        *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
+        const float4* const at = p.part + part_at(ld, row, c, ROWS_LOG2);
+        add_parts(f, at, p.splits, next, ROWS_LOG2);
+        if (GLU) add_parts(g, at + (int64_t)(p.N / 4) * R, p.splits, next, ROWS_LOG2);
+        finish8<EPI, GELU>(p, row, c, f, g);
     }
 }
 
@@ -811,6 +838,9 @@ struct Plan {
     int bn, m_units, n_tiles, kb, splits, a_bytes, b_bytes, stages;
     size_t part_bytes;
 };
+
+// log2 of the rows of a block of partial sums
+int part_rows_log2(int64_t M) { return M > 1 << PART_ROWS_LOG2 ? PART_ROWS_LOG2 : 0; }
 
 // M x N outputs (N: channels of GLU) over a contraction of kb stages: the cut
 // with the least time by these rates (us; measured, see the header):
@@ -845,7 +875,7 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
                 best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages,
-                            splits > 1 ? align256((size_t)splits * M * cols * 4) : 0};
+                            splits > 1 ? align256((size_t)splits * part_size(M, (int)cols, part_rows_log2(M)) * 16) : 0};
             }
         }
     }
@@ -937,7 +967,7 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
 // call (it may run beside them, unless it needs the shared partial sums).
 template <int EPI, bool AMN, bool BMN, bool F8 = false>
 cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                    FfnParams p, float* part, const char* name, bool after, cudaStream_t s, bool independent = false) {
+                    FfnParams p, float4* part, const char* name, bool after, cudaStream_t s, bool independent = false) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int kstep = F8 ? 128 : 64;
     const Plan pl = make_plan(c, M, N, (int)((K + kstep - 1) / kstep), GLU, EPI == EPI_DGLU, AMN, BMN);
@@ -956,6 +986,7 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     p.late_wait = independent && pdl && pl.splits == 1;
     p.status = c->d_status;
     p.part = part;
+    p.part_rows = part_rows_log2(M);
     p.b_rows = GLU || pl.pair ? pl.bn / 2 : pl.bn;
     // fp32 accumulator; formats bf16 (or E4M3: 0); MN-major bits; N / 8; M / 16
     p.idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
@@ -981,10 +1012,11 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     prof_end(c, s);
     if (e == cudaSuccess && pl.splits > 1) {
         prof_begin(c, s, "ffn_join");
-        const int64_t threads = M * (N / 8);
+        const int64_t threads = part_size(M, (int)N, p.part_rows) / 2;
         const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
-        e = gelu ? launch_after(c, ffn_join_kernel<EPI, ACT>, blocks, dim3(256), 0, s, p)
-                 : launch_after(c, ffn_join_kernel<EPI, false>, blocks, dim3(256), 0, s, p);
+        auto join = [&](auto* kernel) { return launch_after(c, kernel, blocks, dim3(256), 0, s, p); };
+        e = p.part_rows ? (gelu ? join(ffn_join_kernel<EPI, ACT, PART_ROWS_LOG2>) : join(ffn_join_kernel<EPI, false, PART_ROWS_LOG2>))
+                        : (gelu ? join(ffn_join_kernel<EPI, ACT, 0>) : join(ffn_join_kernel<EPI, false, 0>));
         prof_end(c, s);
     }
     return e;
@@ -1010,7 +1042,7 @@ Saved saved_of(const void* base, int64_t n, int64_t f) {
 // Scratch: the products' shared partial sums, then the intermediate matrix
 // (forward: a [n][f], unless it is saved; backward: dg and du [n][2f]).
 struct FfnWs {
-    float* part;
+    float4* part;
     __nv_bfloat16* mid;
     size_t bytes;
 };
@@ -1036,7 +1068,7 @@ FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad
         p += align256(bytes);
         return q;
     };
-    w.part = reinterpret_cast<float*>(take(part));
+    w.part = reinterpret_cast<float4*>(take(part));
     w.mid = reinterpret_cast<__nv_bfloat16*>(take((size_t)n * pitch(grad ? 2 * f : f) * 2));
     w.bytes = (size_t)(p - static_cast<char*>(base));
     return w;
