@@ -17,6 +17,11 @@
 //   EPI_OUT    bf16 output, residual added in fp32 before the one rounding
 //   EPI_PART   fp32 partial sums of a split contraction (few rows: the
 //              weights are read once, by all SMs), joined by a second kernel
+// MIXED: waves of whole tiles; the stages of the tiles that do not fill a wave
+// are dealt out evenly, in order, and a tile that several workers share leaves
+// partial sums for the join (2048 rows, d 2560, f 10240, whose down projection
+// has 80 tiles for 74 pairs: 247 us with two waves, 226 so; with the backward
+// 791 and 725; n 4952, d 808, f 3232 with the backward 299 and 279).
 // An operand whose contraction index is the row of its matrix (Wd in da, Wgu
 // in dx, both in the weight gradients) is loaded as it lies and multiplied
 // MN-major: nothing is transposed in memory.
@@ -87,6 +92,7 @@ struct FfnParams {
     int kb;                     // stages along the contraction
     int bn;                     // accumulator columns per tile (EPI_GLU: gate and up together)
     int n_tiles, m_units, splits, raster;
+    int full, dealt, shares;    // MIXED: tiles computed whole, workers the others are dealt to, partial sums per tile at most
     uint32_t idesc;
     int a_bytes, b_bytes;       // of a stage
     int stages;
@@ -98,8 +104,8 @@ struct FfnParams {
     const __nv_bfloat16* res;   // OUT: [M][N] or null
     const float* row_scale;     // FP8: [M]
     const float* col_scale;     // FP8: [2N]
-    float4* part;               // PART: [splits] of a matrix [M][N] (GLU: [M][2N]): see part_at
-    int part_rows;              // log2 of its block's rows
+    float4* part;               // PART: [splits] of a matrix [M][N] (GLU: [M][2N]); MIXED: [tiles][shares] of [256][bn]; see part_at
+    int part_rows;              // PART: log2 of its block's rows
     uint32_t* status;
     int late_wait;              // nothing here depends on the kernel before: wait for it only before leaving
     int stall;                  // test hook: CTA 0 announces its first B stage but never loads it
@@ -275,6 +281,29 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// ---------------------------------------------------------------- work of a CTA or pair
+
+// Row unit and column tile of tile t: groups of `raster` row units share the
+// columns' slice of B while it is in L2.
+__device__ __forceinline__ void place(const FfnParams& p, int t, int& row, int& nt) {
+    const int per = p.raster * p.n_tiles;
+    const int g = t / per, local = t - g * per;
+    const int rows_g = min(p.raster, p.m_units - g * p.raster);
+    row = g * p.raster + local % rows_g;
+    nt = local / rows_g;
+}
+
+// MIXED: the stages of the tiles behind the first `full`, numbered through, are
+// dealt to `dealt` workers: worker w has [w T / dealt, (w + 1) T / dealt).
+__device__ __forceinline__ int64_t dealt_stages(const FfnParams& p) {
+    return (int64_t)(p.n_tiles * p.m_units - p.full) * p.kb;
+}
+__device__ __forceinline__ int64_t deal_lo(const FfnParams& p, int64_t T, int w) { return w * T / p.dealt; }
+// the worker that has stage x
+__device__ __forceinline__ int deal_of(const FfnParams& p, int64_t T, int64_t x) {
+    return (int)(((x + 1) * p.dealt - 1) / T);
+}
+
 // Partial sums lie four columns an element, [row / R][column / 4][row % R]; R is
 // 32 where there are more rows: a warp's rows are contiguous where they are
 // written and read (d 2560, f 10240: 128 rows 44.9 us with R = 1, 41.5 with 32;
@@ -299,11 +328,18 @@ __device__ __forceinline__ void add_parts(float* acc, const float4* at, int n, i
     }
 }
 
+struct Work {
+    int row, nt;        // row unit, column tile
+    int klo, khi;       // stages
+    int split;          // PART
+    int slot;           // MIXED: where the partial sums go, or -1: the whole tile
+};
+
 // ---------------------------------------------------------------- kernel
 
 // AMN / BMN: the operand is MN-major (contraction index = row of its matrix).
 // GLU: B's two column halves are the gate and up rows of the same channels.
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED>
 __global__ void __launch_bounds__(THREADS, 1)
 ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
     constexpr int NCTA = PAIR ? 2 : 1;
@@ -362,21 +398,46 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     const uint32_t tmem_base = sb->tmem_base;
     grid_dep_launch_dependents();
 
-    // unit -> split, row unit and column tile; groups of `raster` row units
-    // share the columns' slice of B while it is in L2
-    struct Where {
-        int split, row, nt;
+    // this worker's units one after the other: every role walks the same list
+    struct Cursor {
+        int u;
+        int64_t pos, end;
     };
-    auto where = [&](int u) {
-        Where w;
-        w.split = u / tiles;
-        const int t = u - w.split * tiles;
-        const int per = p.raster * p.n_tiles;
-        const int g = t / per, local = t - g * per;
-        const int rows_g = min(p.raster, p.m_units - g * p.raster);
-        w.row = g * p.raster + local % rows_g;
-        w.nt = local / rows_g;
-        return w;
+    const int64_t T = MIXED ? dealt_stages(p) : 0;
+    auto begin = [&]() {
+        Cursor c{unit0, 0, 0};
+        if (MIXED && unit0 < p.dealt) {
+            c.pos = deal_lo(p, T, unit0);
+            c.end = deal_lo(p, T, unit0 + 1);
+        }
+        return c;
+    };
+    auto next = [&](Cursor& c, Work& w) {
+        w.split = 0;
+        w.slot = -1;
+        w.klo = 0;
+        w.khi = p.kb;
+        if (!MIXED) {
+            if (c.u >= num_units) return false;
+            w.split = c.u / tiles;
+            place(p, c.u - w.split * tiles, w.row, w.nt);
+            w.klo = (int)((int64_t)p.kb * w.split / p.splits);
+            w.khi = (int)((int64_t)p.kb * (w.split + 1) / p.splits);
+        } else if (c.u < p.full) {
+            place(p, c.u, w.row, w.nt);
+        } else {
+            if (c.pos >= c.end) return false;
+            const int tt = (int)(c.pos / p.kb);
+            const int64_t t0 = (int64_t)tt * p.kb;
+            w.klo = (int)(c.pos - t0);
+            w.khi = (int)min((int64_t)p.kb, c.end - t0);
+            place(p, p.full + tt, w.row, w.nt);
+            if (w.klo != 0 || w.khi != p.kb) w.slot = tt * p.shares + unit0 - deal_of(p, T, t0);
+            c.pos = t0 + w.khi;
+            return true;
+        }
+        c.u += step;
+        return true;
     };
     // bytes of B that producer `part` loads a stage: 64-column boxes in turn
     auto b_share = [&](int part) {
@@ -384,7 +445,6 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         const int boxes = p.b_bytes / (BK * ROWB);
         return (boxes + 1 - part) / 2 * (BK * ROWB);
     };
-    auto k_lo = [&](int split) { return (int)((int64_t)p.kb * split / p.splits); };
 
     if (warp == 0 || warp == 2 || (AMN && warp == 3) || (BMN && warp == 4)) {
         // ---------------- TMA producers, one load a stage each where it can
@@ -402,12 +462,11 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             if (is_a && !p.late_wait) grid_dep_wait();
             int it = 0, s = 0;
             uint32_t ph = 0;
-            for (int u = unit0; u < num_units && !sb->abort_flag; u += step) {
-                const Where w = where(u);
+            Work w;
+            for (Cursor cur = begin(); !sb->abort_flag && next(cur, w);) {
                 const int m0 = (w.row * NCTA + (int)rank) * BM;
-                const int kend = k_lo(w.split + 1);
                 bool ok = true;
-                for (int kb = k_lo(w.split); kb < kend; ++kb, ++it) {
+                for (int kb = w.klo; kb < w.khi; ++kb, ++it) {
                     if (!wait_bounded(&sb->empty[s], ph ^ 1u, sb, p.status)) {
                         ok = false;
                         break;
@@ -453,16 +512,15 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         if (lane == 0) {
             int it = 0, tc = 0, s = 0;
             uint32_t ph = 0;
-            for (int u = unit0; u < num_units && !sb->abort_flag; u += step, ++tc) {
-                const Where w = where(u);
+            Work w;
+            for (Cursor cur = begin(); !sb->abort_flag && next(cur, w); ++tc) {
                 const int acc = tc & 1;
                 const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
                 if (!wait_bounded(&sb->tempty[acc], aph ^ 1u, sb, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * MAX_BN);
-                const int klo = k_lo(w.split), kend = k_lo(w.split + 1);
                 bool ok = true;
-                for (int kb = klo; kb < kend; ++kb, ++it) {
+                for (int kb = w.klo; kb < w.khi; ++kb, ++it) {
                     if (!wait_bounded(&sb->full[s], ph, sb, p.status)) {
                         ok = false;
                         break;
@@ -475,7 +533,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     for (int kk = 0; kk < 4; ++kk) {
                         // 16 contraction indices: 32 bytes inside the swizzled row, or 16 rows of 128 bytes
                         umma<PAIR, F8>(d_tmem, da + (uint64_t)(kk * (AMN ? 128 : 2)), db + (uint64_t)(kk * (BMN ? 128 : 2)),
-                                       p.idesc, (uint32_t)((kb != klo) | (kk != 0)));
+                                       p.idesc, (uint32_t)((kb != w.klo) | (kk != 0)));
                     }
                     if constexpr (PAIR) umma_commit_pair_both(&sb->empty[s]);
                     else umma_commit(&sb->empty[s]);
@@ -518,11 +576,11 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         int in_sent = 0, in_used = 0;
         const uint64_t in_policy = l2_policy_evict_first();
         // columns of g (and of u) of block b of unit u that this warp reads: 0 where there is nothing
-        auto in_cols = [&](const Where& w, int b) {
+        auto in_cols = [&](const Work& w, int b) {
             const int64_t row0 = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32;
-            return row0 < p.M ? max(0, min(32, p.N - (w.nt * p.bn + b))) : 0;
+            return row0 < p.M && w.slot < 0 ? max(0, min(32, p.N - (w.nt * p.bn + b))) : 0;
         };
-        auto in_copy = [&](const Where& w, int b) {
+        auto in_copy = [&](const Work& w, int b) {
             const int cols = in_cols(w, b);
             if (cols == 0) return;
             if (lane == 0) {
@@ -539,11 +597,13 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             }
             ++in_sent;
         };
-        if constexpr (BULK) {
-            if (unit0 < num_units) in_copy(where(unit0), part * 32);
-        }
-        for (int u = unit0; u < num_units; u += step, ++tc) {
-            const Where w = where(u);
+        Work w, ahead;
+        Cursor cur = begin();
+        bool more = next(cur, ahead);
+        if (BULK && more) in_copy(ahead, part * 32);
+        for (; more; ++tc) {
+            w = ahead;
+            more = next(cur, ahead);
             const int acc = tc & 1;
             const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
             const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
@@ -578,7 +638,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 for (int b = part * 32; b < p.bn; b += 32 * EPI_PARTS) {
                     // the next block: of this tile, or the first of the next one
                     if (b + 32 * EPI_PARTS < p.bn) in_copy(w, b + 32 * EPI_PARTS);
-                    else if (u + step < num_units) in_copy(where(u + step), part * 32);
+                    else if (more) in_copy(ahead, part * 32);
                     const int cols = in_cols(w, b);
                     if (cols == 0) continue;
                     const uint8_t* from = in_buf + (in_used & 1) * IN_BUF + lane * 16;
@@ -634,6 +694,24 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 }
                 if (!__all_sync(0xffffffffu, in_ok)) break;
             }
+            if (MIXED && w.slot >= 0) {
+                // a share of the tile: the accumulator's columns as they are
+                float4* const to = p.part + w.slot * part_size(2 * BM, p.bn, PART_ROWS_LOG2) +
+                                   part_at(p.bn, (int)rank * BM + q * 32 + lane, 0, PART_ROWS_LOG2);
+#pragma unroll 1
+                for (int c = part * 16; c < p.bn; c += 16 * EPI_PARTS) {
+                    uint32_t x[16];
+                    tmem_ld16(taddr + c, x);
+                    tmem_wait_ld(x);
+                    if (live) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            to[(c + k) * 8] = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
+                                                          __uint_as_float(x[k + 3]));
+                    }
+                    __syncwarp();
+                }
+            }
             // the patch's lane: row r of four, 16-byte chunk lane % 8
             auto each_line = [&](int b0, auto&& f) {
 #pragma unroll
@@ -644,7 +722,9 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (to_row < p.M && b0 + ch * 8 < width && col < p.N) f(r, ch, to_row, col);
                 }
             };
-            const int nk = BULK ? 0 : STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4 : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
+            const int nk = BULK || (MIXED && w.slot >= 0) ? 0
+                           : STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4
+                                    : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
 #pragma unroll 1
             for (int k2 = 0; k2 < nk; k2 += 2) {
 #pragma unroll
@@ -772,9 +852,17 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     }
 }
 
-// The epilogue of eight columns whose sums are complete.
-template <int EPI, bool GELU>
+// The epilogue of eight columns whose sums are complete but for the FP8 scales.
+template <int EPI, bool F8, bool GELU>
 __device__ __forceinline__ void finish8(const FfnParams& p, int64_t row, int c, float* f, float* g) {
+    if constexpr (F8) {
+        const float rs = p.row_scale[row];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            f[k] *= rs * p.col_scale[c + k];
+            g[k] *= rs * p.col_scale[p.N + c + k];
+        }
+    }
     if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
     if constexpr (EPI == EPI_DGLU) {
         Raw24 rg, ru;
@@ -789,8 +877,9 @@ __device__ __forceinline__ void finish8(const FfnParams& p, int64_t row, int c, 
     *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
 }
 
-// The partial sums of a split contraction in split order, then the epilogue: a
-// thread takes eight columns of a row, its neighbours the block's other rows.
+// The partial sums of a split contraction in split order, then the epilogue
+// (PART applied the FP8 scales): a thread takes eight columns of a row, its
+// neighbours the block's other rows.
 template <int EPI, bool GELU, int ROWS_LOG2>
 __global__ void ffn_join_kernel(const FfnParams p) {
     constexpr bool GLU = EPI == EPI_GLU;
@@ -807,7 +896,35 @@ __global__ void ffn_join_kernel(const FfnParams p) {
         const float4* const at = p.part + part_at(ld, row, c, ROWS_LOG2);
         add_parts(f, at, p.splits, next, ROWS_LOG2);
         if (GLU) add_parts(g, at + (int64_t)(p.N / 4) * R, p.splits, next, ROWS_LOG2);
-        finish8<EPI, GELU>(p, row, c, f, g);
+        finish8<EPI, false, GELU>(p, row, c, f, g);
+    }
+}
+
+// MIXED: the tiles that several workers share, the shares in stage order.
+template <int EPI, bool F8, bool GELU>
+__global__ void ffn_join_mixed_kernel(const FfnParams p) {
+    constexpr bool GLU = EPI == EPI_GLU;
+    const int width = GLU ? p.bn / 2 : p.bn, vec = width / 8;
+    const int64_t T = dealt_stages(p), next = part_size(2 * BM, p.bn, PART_ROWS_LOG2);
+    const int64_t total = (int64_t)(p.n_tiles * p.m_units - p.full) * (2 * BM) * vec;
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        // lane: row within 32; then column group, row block, tile
+        const int64_t j = i >> 5;
+        const int v = (int)(j % vec), rb = (int)(j / vec % (2 * BM / 32)), tt = (int)(j / vec / (2 * BM / 32));
+        const int first = deal_of(p, T, (int64_t)tt * p.kb);
+        const int n = deal_of(p, T, (int64_t)(tt + 1) * p.kb - 1) - first + 1;
+        int unit, nt;
+        place(p, p.full + tt, unit, nt);
+        const int ur = rb * 32 + (int)(i & 31), c = nt * width + v * 8;
+        const int64_t row = (int64_t)unit * (2 * BM) + ur;
+        if (n == 1 || row >= p.M || c >= p.N) continue;    // one worker: done there
+        float f[8] = {}, g[8] = {};
+        const float4* const at = p.part + (int64_t)tt * p.shares * next + part_at(p.bn, ur, v * 8, PART_ROWS_LOG2);
+        add_parts(f, at, n, next, PART_ROWS_LOG2);
+        if (GLU) add_parts(g, at + width * 8, n, next, PART_ROWS_LOG2);
+        finish8<EPI, F8, GELU>(p, row, c, f, g);
     }
 }
 
@@ -836,6 +953,7 @@ int64_t pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 struct Plan {
     bool pair;
     int bn, m_units, n_tiles, kb, splits, a_bytes, b_bytes, stages;
+    int full, dealt, shares;    // MIXED (dealt > 0)
     size_t part_bytes;
 };
 
@@ -845,9 +963,13 @@ int part_rows_log2(int64_t M) { return M > 1 << PART_ROWS_LOG2 ? PART_ROWS_LOG2 
 // M x N outputs (N: channels of GLU) over a contraction of kb stages: the cut
 // with the least time by these rates (us; measured, see the header):
 //   a stage   the larger of its MMAs, the ring's round trip over its stages,
-//             and its bytes into one SM
+//             and its bytes into one SM (full waves of pairs, several row units:
+//             0.29 us at 64 columns, 0.32 at 128, 0.35 from 160 to 256)
 //   all       the weights from HBM
-//   a split   the partial sums written and read back, and the join's launch
+//   a split, a share   the partial sums written and read back, and the join's launch
+// Dealt stages are taken where they save a twentieth.  Not for one row unit,
+// whose time is the weights' (256 rows, d 2560, f 10240: 55 us, with them 57),
+// nor behind four waves (16384 rows 1666 us, with them 1706).
 Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu, bool amn, bool bmn) {
     Plan best{};
     double best_cost = 1e30;
@@ -865,7 +987,9 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
         const int a_bytes = a_rows * ROWB, b_bytes = (pair ? bn / 2 : bn) * ROWB;
         // the MMA reads 128 rows of A whatever was staged: the last stage's lie inside the ring too
         const int stages = std::min(MAX_STAGES, (TILE_AREA - keep - (A_BYTES - a_bytes)) / (a_bytes + b_bytes));
-        const double stage = std::max(std::max(0.365 * bn / 256, 1.4 / stages), (a_bytes + b_bytes) / 80e3);
+        const double bytes = (a_bytes + b_bytes) / 80e3;
+        const double stage = std::max(std::max(0.365 * bn / 256, 1.4 / stages),
+                                      m_units > 1 ? std::min(0.03 + bytes, 0.355) : bytes);
         for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
             if (splits > 1 && tiles * (splits - 1) >= workers) break;
             const int64_t waves = (tiles * splits + workers - 1) / workers;
@@ -874,8 +998,27 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
             if (splits > 1) cost += 3.0 + (double)splits * M * cols * 8 / 6e6;
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
-                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages,
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages, 0, 0, 0,
                             splits > 1 ? align256((size_t)splits * part_size(M, (int)cols, part_rows_log2(M)) * 16) : 0};
+            }
+        }
+        // whole waves, then the other tiles' stages dealt to all workers or to a few per tile
+        const int64_t full = tiles / workers * workers, tail = tiles - full;
+        for (int per_tile = 1; m_units > 1 && tail > 0 && full + tail < 4 * workers && per_tile <= 16; ++per_tile) {
+            const int64_t dealt = per_tile == 1 ? workers : tail * per_tile;
+            const int64_t total = tail * kb;
+            if (dealt > workers || dealt <= tail || total < 4 * dealt) continue;
+            const int64_t each = (total + dealt - 1) / dealt, shares = (kb + total / dealt - 1) / (total / dealt) + 1;
+            const double units = ((double)(full / workers) * kb + each) * stage;
+            // workers are at different stages: operands that L2 does not hold are read by each of them
+            const bool shared = (double)kb * ROWB * (cols + M) < 1e8;
+            const double hbm = (shared ? (double)kb * ROWB * cols : (double)total * 2 * (a_bytes + b_bytes)) / 6.4e6;
+            const double cost = 1.05 * (std::max(units, hbm) + 0.2 * std::min(units, hbm) + 4.0 +
+                                       (double)(dealt + tail) * std::min<int64_t>(M, 2 * BM) * bn * 8 / 6e6);
+            if (cost < best_cost * 0.98) {
+                best_cost = cost;
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, 1, a_bytes, b_bytes, stages, (int)full, (int)dealt, (int)shares,
+                            align256((size_t)tail * shares * 2 * BM * bn * 4)};
             }
         }
     }
@@ -907,10 +1050,10 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     return e.plan;
 }
 
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED = false>
 cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, bool pdl,
                        cudaStream_t s) {
-    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU>;
+    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU, MIXED>;
     static std::mutex mu;
     static int max_units[64] = {};              // CTAs or pairs resident at once, per device
     int dev = 0;
@@ -950,7 +1093,9 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
     }
     const int64_t units = (int64_t)p.m_units * p.n_tiles * p.splits;
     if (units >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) * std::min<int64_t>(units, cap)), 1, 1);
+    // MIXED: every worker that stages are dealt to has to be there, resident at once or not
+    const int64_t grid = MIXED ? std::max<int64_t>(num_sms / 2, p.dealt) : std::min<int64_t>(units, cap);
+    cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) * grid), 1, 1);
     if (pdl) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
@@ -983,7 +1128,10 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     p.b_bytes = pl.b_bytes;
     p.stages = pl.stages;
     p.raster = 8;
-    p.late_wait = independent && pdl && pl.splits == 1;
+    p.late_wait = independent && pdl && pl.splits == 1 && pl.dealt == 0;
+    p.full = pl.full;
+    p.dealt = pl.dealt;
+    p.shares = pl.shares;
     p.status = c->d_status;
     p.part = part;
     p.part_rows = part_rows_log2(M);
@@ -1000,7 +1148,10 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     cudaError_t e;
     constexpr bool ACT = EPI == EPI_GLU || EPI == EPI_DGLU;
     const bool gelu = ACT && p.act == ENGRAM_ACT_GELU;
-    if (pl.splits > 1)
+    if (pl.dealt > 0)
+        e = gelu ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT, true>(ma, mb, p, c->num_sms, pdl, s)
+                 : launch_one<EPI, GLU, AMN, BMN, true, F8, false, true>(ma, mb, p, c->num_sms, pdl, s);
+    else if (pl.splits > 1)
         e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
                     : launch_one<EPI_PART, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
     else if (gelu)
@@ -1010,6 +1161,14 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
         e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
                     : launch_one<EPI, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
     prof_end(c, s);
+    if (e == cudaSuccess && pl.dealt > 0) {
+        prof_begin(c, s, "ffn_join");
+        const int64_t threads = ((int64_t)pl.n_tiles * pl.m_units - pl.full) * (2 * BM) * ((GLU ? pl.bn / 2 : pl.bn) / 8);
+        const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
+        e = gelu ? launch_after(c, ffn_join_mixed_kernel<EPI, F8, ACT>, blocks, dim3(256), 0, s, p)
+                 : launch_after(c, ffn_join_mixed_kernel<EPI, F8, false>, blocks, dim3(256), 0, s, p);
+        prof_end(c, s);
+    }
     if (e == cudaSuccess && pl.splits > 1) {
         prof_begin(c, s, "ffn_join");
         const int64_t threads = part_size(M, (int)N, p.part_rows) / 2;

@@ -130,6 +130,22 @@ def test_ffn_grad(eb, n, d, f, kind):
     assert all(torch.equal(p, q) for p, q in zip(got, again))
 
 
+# Tiles that do not fill a wave of SM pairs, each product's in turn: their contraction is shared among pairs, with
+# and without whole waves before them.
+@pytest.mark.parametrize("n,d,f", [(6389, 2504, 296), (6654, 264, 4936), (6275, 536, 1504), (399, 1400, 9648),
+                                   (6240, 144, 6328)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_ffn_shared_tiles(eb, n, d, f, kind):
+    test_ffn(eb, n, d, f, kind, kind == "gelu")
+    test_ffn_grad(eb, n, d, f, kind)
+
+
+@pytest.mark.parametrize("n,d,f", [(6389, 2560, 296), (6240, 128, 6328)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_ffn_shared_tiles_fp8(eb, n, d, f, kind):
+    test_ffn_fp8(eb, n, d, f, kind)
+
+
 @pytest.mark.parametrize("n", [1, 5, 300])
 def test_ffn_products_are_exact_on_small_integers(eb, n):
     """Gates far above zero (act(g) = g to fp32) and small integers make every product exact: a row, column or
