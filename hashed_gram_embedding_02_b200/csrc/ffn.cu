@@ -22,6 +22,11 @@
 // partial sums for the join (2048 rows, d 2560, f 10240, whose down projection
 // has 80 tiles for 74 pairs: 247 us with two waves, 226 so; with the backward
 // 791 and 725; n 4952, d 808, f 3232 with the backward 299 and 279).
+// DUAL: a pair takes two neighbouring gate and up tiles at once, an accumulator
+// each, and reads a stage of x once for both: where one wave of such holds all
+// (256 rows, d 2560, f 10240: 55.0 us with two waves, 52.8 so; 700 rows, d 2048,
+// f 4096, 46.1 and 43.3; not where less than that is saved: E4M3, 1000 rows,
+// d 1024, f 2816, 30.5 and 32.1).
 // An operand whose contraction index is the row of its matrix (Wd in da, Wgu
 // in dx, both in the weight gradients) is loaded as it lies and multiplied
 // MN-major: nothing is transposed in memory.
@@ -339,7 +344,7 @@ struct Work {
 
 // AMN / BMN: the operand is MN-major (contraction index = row of its matrix).
 // GLU: B's two column halves are the gate and up rows of the same channels.
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED, bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1)
 ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
     constexpr int NCTA = PAIR ? 2 : 1;
@@ -492,7 +497,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         for (int c = part * 64; c < cols; c += 128) load(&map_b, b_dst + c * ROWB, n0 + c, k0);
                     } else if constexpr (GLU) {
                         // gate rows from nt * bn / 2, up rows N behind; a pair's second CTA stages the up rows
-                        const int n0 = w.nt * (p.bn / 2);
+                        const int n0 = w.nt * p.b_rows;
                         load(&map_b, b_dst, k0, n0 + (PAIR ? (int)rank * p.N : 0));
                         if (!PAIR) load(&map_b, b_dst + p.b_rows * ROWB, k0, n0 + p.N);
                     } else {
@@ -513,10 +518,11 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             int it = 0, tc = 0, s = 0;
             uint32_t ph = 0;
             Work w;
-            for (Cursor cur = begin(); !sb->abort_flag && next(cur, w); ++tc) {
+            for (Cursor cur = begin(); !sb->abort_flag && next(cur, w); tc += DUAL ? 2 : 1) {
                 const int acc = tc & 1;
                 const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
                 if (!wait_bounded(&sb->tempty[acc], aph ^ 1u, sb, p.status)) break;
+                if (DUAL && !wait_bounded(&sb->tempty[1], aph ^ 1u, sb, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * MAX_BN);
                 bool ok = true;
@@ -534,6 +540,9 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         // 16 contraction indices: 32 bytes inside the swizzled row, or 16 rows of 128 bytes
                         umma<PAIR, F8>(d_tmem, da + (uint64_t)(kk * (AMN ? 128 : 2)), db + (uint64_t)(kk * (BMN ? 128 : 2)),
                                        p.idesc, (uint32_t)((kb != w.klo) | (kk != 0)));
+                        if constexpr (DUAL)
+                            umma<PAIR, F8>(d_tmem + MAX_BN, da + (uint64_t)(kk * 2), db + (uint64_t)(p.b_bytes / 32 + kk * 2), p.idesc,
+                                           (uint32_t)((kb != w.klo) | (kk != 0)));
                     }
                     if constexpr (PAIR) umma_commit_pair_both(&sb->empty[s]);
                     else umma_commit(&sb->empty[s]);
@@ -546,6 +555,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 if (!ok) break;
                 if constexpr (PAIR) umma_commit_pair_both(&sb->tfull[acc]);
                 else umma_commit(&sb->tfull[acc]);
+                if constexpr (DUAL) umma_commit_pair_both(&sb->tfull[1]);
             }
         }
     } else if (warp >= EPI_WARP0) {
@@ -601,9 +611,14 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         Cursor cur = begin();
         bool more = next(cur, ahead);
         if (BULK && more) in_copy(ahead, part * 32);
-        for (; more; ++tc) {
-            w = ahead;
-            more = next(cur, ahead);
+        for (; more || (DUAL && tc & 1); ++tc) {
+            if (DUAL && tc & 1) {
+                ++w.nt;
+            } else {
+                w = ahead;
+                if (DUAL) w.nt *= 2;
+                more = next(cur, ahead);
+            }
             const int acc = tc & 1;
             const uint32_t aph = (uint32_t)(tc >> 1) & 1u;
             const int64_t row = (int64_t)(w.row * NCTA + (int)rank) * BM + q * 32 + lane;
@@ -953,6 +968,7 @@ int64_t pitch(int64_t cols) { return (cols + 63) / 64 * 64; }
 struct Plan {
     bool pair;
     int bn, m_units, n_tiles, kb, splits, a_bytes, b_bytes, stages;
+    int dual;                   // two column tiles at once (n_tiles counts them as one)
     int full, dealt, shares;    // MIXED (dealt > 0)
     size_t part_bytes;
 };
@@ -998,8 +1014,20 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
             if (splits > 1) cost += 3.0 + (double)splits * M * cols * 8 / 6e6;
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
-                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages, 0, 0, 0,
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages, 0, 0, 0, 0,
                             splits > 1 ? align256((size_t)splits * part_size(M, (int)cols, part_rows_log2(M)) * 16) : 0};
+            }
+        }
+        // two column tiles at once, in one wave: A is read once for both; both epilogues come behind all MMAs (4 us)
+        const int64_t twos = m_units * ((n_tiles + 1) / 2);
+        if (glu && pair && n_tiles > 1 && twos <= workers) {
+            const int ring = std::min(MAX_STAGES, (TILE_AREA - keep) / (a_bytes + 2 * b_bytes));
+            const double units = kb * std::max(std::max(0.365 * bn / 128, 1.4 / ring), (a_bytes + 2 * b_bytes) / 80e3);
+            const double hbm = (double)kb * ROWB * cols / 6.4e6;
+            const double cost = std::max(units, hbm) + 0.2 * std::min(units, hbm) + 4.0;
+            if (cost < best_cost * 0.98) {
+                best_cost = cost;
+                best = Plan{pair, bn, (int)m_units, (int)((n_tiles + 1) / 2), kb, 1, a_bytes, 2 * b_bytes, ring, 1, 0, 0, 0, 0};
             }
         }
         // whole waves, then the other tiles' stages dealt to all workers or to a few per tile
@@ -1017,7 +1045,7 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
                                        (double)(dealt + tail) * std::min<int64_t>(M, 2 * BM) * bn * 8 / 6e6);
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
-                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, 1, a_bytes, b_bytes, stages, (int)full, (int)dealt, (int)shares,
+                best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, 1, a_bytes, b_bytes, stages, 0, (int)full, (int)dealt, (int)shares,
                             align256((size_t)tail * shares * 2 * BM * bn * 4)};
             }
         }
@@ -1050,10 +1078,10 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     return e.plan;
 }
 
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED = false>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED = false, bool DUAL = false>
 cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, bool pdl,
                        cudaStream_t s) {
-    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU, MIXED>;
+    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU, MIXED, DUAL>;
     static std::mutex mu;
     static int max_units[64] = {};              // CTAs or pairs resident at once, per device
     int dev = 0;
@@ -1135,7 +1163,7 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     p.status = c->d_status;
     p.part = part;
     p.part_rows = part_rows_log2(M);
-    p.b_rows = GLU || pl.pair ? pl.bn / 2 : pl.bn;
+    p.b_rows = pl.dual ? pl.bn : GLU || pl.pair ? pl.bn / 2 : pl.bn;
     // fp32 accumulator; formats bf16 (or E4M3: 0); MN-major bits; N / 8; M / 16
     p.idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
               ((uint32_t)(pl.bn >> 3) << 17) | ((uint32_t)((pl.pair ? 256 : 128) >> 4) << 24);
@@ -1148,7 +1176,10 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     cudaError_t e;
     constexpr bool ACT = EPI == EPI_GLU || EPI == EPI_DGLU;
     const bool gelu = ACT && p.act == ENGRAM_ACT_GELU;
-    if (pl.dealt > 0)
+    if (GLU && pl.dual)
+        e = gelu ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT, false, GLU>(ma, mb, p, c->num_sms, pdl, s)
+                 : launch_one<EPI, GLU, AMN, BMN, true, F8, false, false, GLU>(ma, mb, p, c->num_sms, pdl, s);
+    else if (pl.dealt > 0)
         e = gelu ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT, true>(ma, mb, p, c->num_sms, pdl, s)
                  : launch_one<EPI, GLU, AMN, BMN, true, F8, false, true>(ma, mb, p, c->num_sms, pdl, s);
     else if (pl.splits > 1)

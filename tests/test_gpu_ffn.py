@@ -140,7 +140,14 @@ def test_ffn_shared_tiles(eb, n, d, f, kind):
     test_ffn_grad(eb, n, d, f, kind)
 
 
-@pytest.mark.parametrize("n,d,f", [(6389, 2560, 296), (6240, 128, 6328)])
+# Between one and two waves of gate and up tiles: a pair takes two at once; the last pair of an odd number has one.
+@pytest.mark.parametrize("n,d,f", [(200, 2560, 10240), (512, 2560, 5000), (700, 2048, 4096)])
+@pytest.mark.parametrize("kind,with_res", [("silu", True), ("gelu", False)])
+def test_ffn_two_tiles_at_once(eb, n, d, f, kind, with_res):
+    test_ffn(eb, n, d, f, kind, with_res)
+
+
+@pytest.mark.parametrize("n,d,f", [(6389, 2560, 296), (6240, 128, 6328), (300, 4096, 6000)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_ffn_shared_tiles_fp8(eb, n, d, f, kind):
     test_ffn_fp8(eb, n, d, f, kind)
