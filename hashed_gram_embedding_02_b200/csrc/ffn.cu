@@ -15,8 +15,13 @@
 //   EPI_DGLU   da in the accumulator; the epilogue reads g and u and writes
 //              dg and du
 //   EPI_OUT    bf16 output, residual added in fp32 before the one rounding
-//   EPI_PART   fp32 partial sums of a split contraction (few rows: the
-//              weights are read once, by all SMs), joined by a second kernel
+//   EPI_PART   fp32 partial sums of a split contraction (few tiles: the
+//              operands are read by all SMs), joined by a second kernel
+// CLUSTER (up to 128 rows): the CTAs that split a tile's contraction are a
+// cluster and add their sums through shared memory: no second kernel and
+// nothing in global memory (one row, d 1152, f 1456: 19.0 us with partial sums
+// and a join, 14.0 so; 3 rows, d 384, f 1952 in E4M3 17.0 and 11.3; one row,
+// d 2560, f 10240 36.1 and 34.7; at worst 20 rows, d 384, f 7824 15.3 and 16.4).
 // MIXED: waves of whole tiles; the stages of the tiles that do not fill a wave
 // are dealt out evenly, in order, and a tile that several workers share leaves
 // partial sums for the join (2048 rows, d 2560, f 10240, whose down projection
@@ -110,7 +115,6 @@ struct FfnParams {
     const float* row_scale;     // FP8: [M]
     const float* col_scale;     // FP8: [2N]
     float4* part;               // PART: [splits] of a matrix [M][N] (GLU: [M][2N]); MIXED: [tiles][shares] of [256][bn]; see part_at
-    int part_rows;              // PART: log2 of its block's rows
     uint32_t* status;
     int late_wait;              // nothing here depends on the kernel before: wait for it only before leaving
     int stall;                  // test hook: CTA 0 announces its first B stage but never loads it
@@ -309,29 +313,40 @@ __device__ __forceinline__ int deal_of(const FfnParams& p, int64_t T, int64_t x)
     return (int)(((x + 1) * p.dealt - 1) / T);
 }
 
-// Partial sums lie four columns an element, [row / R][column / 4][row % R]; R is
-// 32 where there are more rows: a warp's rows are contiguous where they are
-// written and read (d 2560, f 10240: 128 rows 44.9 us with R = 1, 41.5 with 32;
-// 256 rows 62 and 55; n 615, d 496, f 4952 with its backward 92 and 87).  Up to
-// 32 rows R is 1: blocks cost more than they give where rows are few (one row
-// 35.7 and 38; 7 rows, d 2048, f 8192, 29.5 and 31.8).
-constexpr int PART_ROWS_LOG2 = 5;
-__device__ __forceinline__ int64_t part_at(int cols, int64_t row, int col, int rows_log2) {
-    return (((row >> rows_log2) * (cols / 4) + col / 4) << rows_log2) + (row & ((1 << rows_log2) - 1));
+// Partial sums lie four columns an element, [row / 32][column / 4][row % 32]: a
+// warp's rows are contiguous where they are written and read (d 2560, f 10240,
+// 256 rows: 62 us by rows, 55 so; n 615, d 496, f 4952 with its backward 92
+// and 87).
+__device__ __forceinline__ int64_t part_at(int cols, int64_t row, int col) {
+    return ((row >> 5) * (cols / 4) + col / 4) * 32 + (row & 31);
 }
-__host__ __device__ inline int64_t part_size(int64_t rows, int cols, int rows_log2) {
-    return ((rows + (1 << rows_log2) - 1) >> rows_log2 << rows_log2) * (cols / 4);
+__host__ __device__ inline int64_t part_size(int64_t rows, int cols) { return (rows + 31) / 32 * 32 * (cols / 4); }
+
+__device__ __forceinline__ void add4(float* acc, const float4& a) {
+    acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
 }
 
 // sums of eight columns over n matrices `next` elements apart
-__device__ __forceinline__ void add_parts(float* acc, const float4* at, int n, int64_t next, int rows_log2) {
+__device__ __forceinline__ void add_parts(float* acc, const float4* at, int n, int64_t next) {
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-        const float4 a = at[k * next], b = at[k * next + (1 << rows_log2)];
-        acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-        acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+        add4(acc, at[k * next]);
+        add4(acc + 4, at[k * next + 32]);
     }
 }
+
+constexpr int MAX_CLUSTER = 8;      // CTAs; what every device of the kind takes
+
+enum { WHOLE, SPLIT, MIXED_TAIL, TWO_TILES, CLUSTER };
 
 struct Work {
     int row, nt;        // row unit, column tile
@@ -340,14 +355,40 @@ struct Work {
     int slot;           // MIXED: where the partial sums go, or -1: the whole tile
 };
 
+// The epilogue of eight columns whose sums are complete but for the FP8 scales.
+template <int EPI, bool F8, bool GELU>
+__device__ __forceinline__ void finish8(const FfnParams& p, int64_t row, int c, float* f, float* g) {
+    if constexpr (F8) {
+        const float rs = p.row_scale[row];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            f[k] *= rs * p.col_scale[c + k];
+            g[k] *= rs * p.col_scale[p.N + c + k];
+        }
+    }
+    if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
+    if constexpr (EPI == EPI_DGLU) {
+        Raw24 rg, ru;
+        rg.load(p, at24(p, row, c));
+        ru.load(p, at24(p, row, p.N + c));
+        dglu8<GELU>(rg, ru, f, g);
+        *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
+    }
+    if constexpr (EPI == EPI_OUT) {
+        if (p.res) add8(f, *reinterpret_cast<const uint4*>(p.res + row * p.N + c));
+    }
+    *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
+}
+
 // ---------------------------------------------------------------- kernel
 
 // AMN / BMN: the operand is MN-major (contraction index = row of its matrix).
 // GLU: B's two column halves are the gate and up rows of the same channels.
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED, bool DUAL>
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const FfnParams p) {
     constexpr int NCTA = PAIR ? 2 : 1;
+    constexpr bool MIXED = MODE == MIXED_TAIL, DUAL = MODE == TWO_TILES, CL = MODE == CLUSTER;
     const int STAGES = p.stages;
     const int stage_bytes = p.a_bytes + p.b_bytes;
     constexpr int KSTEP = F8 ? 128 : 64;        // contraction indices per stage
@@ -424,8 +465,8 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         w.khi = p.kb;
         if (!MIXED) {
             if (c.u >= num_units) return false;
-            w.split = c.u / tiles;
-            place(p, c.u - w.split * tiles, w.row, w.nt);
+            w.split = CL ? c.u % p.splits : c.u / tiles;
+            place(p, CL ? c.u / p.splits : c.u - w.split * tiles, w.row, w.nt);
             w.klo = (int)((int64_t)p.kb * w.split / p.splits);
             w.khi = (int)((int64_t)p.kb * (w.split + 1) / p.splits);
         } else if (c.u < p.full) {
@@ -637,7 +678,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     }
                 }
             };
-            if constexpr (EPI == EPI_DGLU && !BULK) {
+            if constexpr (EPI == EPI_DGLU && !BULK && !CL) {
                 fetch(chunk(0), rg[0], ru[0]);
                 fetch(chunk(1), rg[1], ru[1]);
             }
@@ -711,8 +752,8 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             }
             if (MIXED && w.slot >= 0) {
                 // a share of the tile: the accumulator's columns as they are
-                float4* const to = p.part + w.slot * part_size(2 * BM, p.bn, PART_ROWS_LOG2) +
-                                   part_at(p.bn, (int)rank * BM + q * 32 + lane, 0, PART_ROWS_LOG2);
+                float4* const to = p.part + w.slot * part_size(2 * BM, p.bn) +
+                                   part_at(p.bn, (int)rank * BM + q * 32 + lane, 0);
 #pragma unroll 1
                 for (int c = part * 16; c < p.bn; c += 16 * EPI_PARTS) {
                     uint32_t x[16];
@@ -727,6 +768,23 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     __syncwarp();
                 }
             }
+            if constexpr (CL) {
+                // this CTA's share of the sums, [column / 4][row], where the ring was: its MMAs are done
+                float4* const to = reinterpret_cast<float4*>(smem) + q * 32 + lane;
+#pragma unroll 1
+                for (int c = part * 16; c < p.bn; c += 16 * EPI_PARTS) {
+                    uint32_t x[16];
+                    tmem_ld16(taddr + c, x);
+                    tmem_wait_ld(x);
+                    if (live) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            to[(c + k) / 4 * p.M] = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]),
+                                                                __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                    }
+                    __syncwarp();
+                }
+            }
             // the patch's lane: row r of four, 16-byte chunk lane % 8
             auto each_line = [&](int b0, auto&& f) {
 #pragma unroll
@@ -737,7 +795,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (to_row < p.M && b0 + ch * 8 < width && col < p.N) f(r, ch, to_row, col);
                 }
             };
-            const int nk = BULK || (MIXED && w.slot >= 0) ? 0
+            const int nk = BULK || CL || (MIXED && w.slot >= 0) ? 0
                            : STAGED ? (width + 64 * EPI_PARTS - 1) / (64 * EPI_PARTS) * 4
                                     : ((width + 16 * EPI_PARTS - 1) / (16 * EPI_PARTS) + 1) / 2 * 2;
 #pragma unroll 1
@@ -781,14 +839,14 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         }
                         const int ch = (c - b0) / 8 + h;
                         if constexpr (EPI == EPI_PART) {
-                            const int ld = GLU ? 2 * p.N : p.N, R = 1 << p.part_rows;
-                            float4* to = p.part + w.split * part_size(p.M, ld, p.part_rows) + part_at(ld, row, col, p.part_rows);
+                            const int ld = GLU ? 2 * p.N : p.N;
+                            float4* to = p.part + w.split * part_size(p.M, ld) + part_at(ld, row, col);
                             to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                            to[R] = make_float4(f[4], f[5], f[6], f[7]);
+                            to[32] = make_float4(f[4], f[5], f[6], f[7]);
                             if (GLU) {
-                                to += (int64_t)(p.N / 4) * R;
+                                to += (int64_t)p.N * 8;
                                 to[0] = make_float4(g[0], g[1], g[2], g[3]);
-                                to[R] = make_float4(g[4], g[5], g[6], g[7]);
+                                to[32] = make_float4(g[4], g[5], g[6], g[7]);
                             }
                         } else {
                             if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, col, f, g);
@@ -828,6 +886,29 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     // this grid must not complete before the one it depends on: those behind it count on both
     if (p.late_wait) grid_dep_wait();
     __syncthreads();
+    if constexpr (CL) {
+        // every CTA of the tile adds the shares, in split order, of some of its columns and rows
+        cluster_sync_all();
+        const int width = GLU ? p.bn / 2 : p.bn, total = p.M * (width / 8);
+        int unit, nt;
+        place(p, (int)blockIdx.x / p.splits, unit, nt);
+        for (int i = (int)cluster_rank() * THREADS + threadIdx.x; i < total; i += p.splits * THREADS) {
+            const int v = i / p.M, row = i - v * p.M, c = nt * width + v * 8;
+            if (c >= p.N) continue;
+            float f[8] = {}, g[8] = {};
+            const float4* const at = reinterpret_cast<const float4*>(smem) + v * 2 * p.M + row;
+#pragma unroll 4
+            for (int k = 0; k < p.splits; ++k) {
+                add4(f, ld_cluster_f4(peer_addr(at, k)));
+                add4(f + 4, ld_cluster_f4(peer_addr(at + p.M, k)));
+                if constexpr (GLU) {
+                    add4(g, ld_cluster_f4(peer_addr(at + width / 4 * p.M, k)));
+                    add4(g + 4, ld_cluster_f4(peer_addr(at + (width / 4 + 1) * p.M, k)));
+                }
+            }
+            finish8<EPI, F8, GELU>(p, row, c, f, g);
+        }
+    }
     bool aborted = sb->abort_flag != 0;
     if constexpr (PAIR) {
         cluster_sync_all();
@@ -857,7 +938,7 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         }
         __syncthreads();
     }
-    if constexpr (PAIR) cluster_sync_all();
+    if constexpr (PAIR || CL) cluster_sync_all();      // CL: shared memory is read by the others until here
     if (warp == 1) {
         tc_fence_after();
         if constexpr (PAIR)
@@ -867,50 +948,24 @@ ffn_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     }
 }
 
-// The epilogue of eight columns whose sums are complete but for the FP8 scales.
-template <int EPI, bool F8, bool GELU>
-__device__ __forceinline__ void finish8(const FfnParams& p, int64_t row, int c, float* f, float* g) {
-    if constexpr (F8) {
-        const float rs = p.row_scale[row];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            f[k] *= rs * p.col_scale[c + k];
-            g[k] *= rs * p.col_scale[p.N + c + k];
-        }
-    }
-    if constexpr (EPI == EPI_GLU) glu8<GELU>(p, row, c, f, g);
-    if constexpr (EPI == EPI_DGLU) {
-        Raw24 rg, ru;
-        rg.load(p, at24(p, row, c));
-        ru.load(p, at24(p, row, p.N + c));
-        dglu8<GELU>(rg, ru, f, g);
-        *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.N + c) = pack8(g);
-    }
-    if constexpr (EPI == EPI_OUT) {
-        if (p.res) add8(f, *reinterpret_cast<const uint4*>(p.res + row * p.N + c));
-    }
-    *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = pack8(f);
-}
-
 // The partial sums of a split contraction in split order, then the epilogue
 // (PART applied the FP8 scales): a thread takes eight columns of a row, its
 // neighbours the block's other rows.
-template <int EPI, bool GELU, int ROWS_LOG2>
+template <int EPI, bool GELU>
 __global__ void ffn_join_kernel(const FfnParams p) {
     constexpr bool GLU = EPI == EPI_GLU;
-    constexpr int R = 1 << ROWS_LOG2;
     const int vec = p.N / 8, ld = GLU ? 2 * p.N : p.N;
-    const int64_t next = part_size(p.M, ld, ROWS_LOG2), total = part_size(p.M, p.N, ROWS_LOG2) / 2;
+    const int64_t next = part_size(p.M, ld), total = part_size(p.M, p.N) / 2;
     grid_dep_wait();
     grid_dep_launch_dependents();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t j = i >> ROWS_LOG2, block = j / vec, row = block * R + (i & (R - 1));
+        const int64_t j = i >> 5, block = j / vec, row = block * 32 + (i & 31);
         const int c = (int)(j - block * vec) * 8;
         if (row >= p.M) continue;
         float f[8] = {}, g[8] = {};
-        const float4* const at = p.part + part_at(ld, row, c, ROWS_LOG2);
-        add_parts(f, at, p.splits, next, ROWS_LOG2);
-        if (GLU) add_parts(g, at + (int64_t)(p.N / 4) * R, p.splits, next, ROWS_LOG2);
+        const float4* const at = p.part + part_at(ld, row, c);
+        add_parts(f, at, p.splits, next);
+        if (GLU) add_parts(g, at + (int64_t)p.N * 8, p.splits, next);
         finish8<EPI, false, GELU>(p, row, c, f, g);
     }
 }
@@ -920,7 +975,7 @@ template <int EPI, bool F8, bool GELU>
 __global__ void ffn_join_mixed_kernel(const FfnParams p) {
     constexpr bool GLU = EPI == EPI_GLU;
     const int width = GLU ? p.bn / 2 : p.bn, vec = width / 8;
-    const int64_t T = dealt_stages(p), next = part_size(2 * BM, p.bn, PART_ROWS_LOG2);
+    const int64_t T = dealt_stages(p), next = part_size(2 * BM, p.bn);
     const int64_t total = (int64_t)(p.n_tiles * p.m_units - p.full) * (2 * BM) * vec;
     grid_dep_wait();
     grid_dep_launch_dependents();
@@ -936,9 +991,9 @@ __global__ void ffn_join_mixed_kernel(const FfnParams p) {
         const int64_t row = (int64_t)unit * (2 * BM) + ur;
         if (n == 1 || row >= p.M || c >= p.N) continue;    // one worker: done there
         float f[8] = {}, g[8] = {};
-        const float4* const at = p.part + (int64_t)tt * p.shares * next + part_at(p.bn, ur, v * 8, PART_ROWS_LOG2);
-        add_parts(f, at, n, next, PART_ROWS_LOG2);
-        if (GLU) add_parts(g, at + width * 8, n, next, PART_ROWS_LOG2);
+        const float4* const at = p.part + (int64_t)tt * p.shares * next + part_at(p.bn, ur, v * 8);
+        add_parts(f, at, n, next);
+        if (GLU) add_parts(g, at + width * 8, n, next);
         finish8<EPI, F8, GELU>(p, row, c, f, g);
     }
 }
@@ -973,8 +1028,7 @@ struct Plan {
     size_t part_bytes;
 };
 
-// log2 of the rows of a block of partial sums
-int part_rows_log2(int64_t M) { return M > 1 << PART_ROWS_LOG2 ? PART_ROWS_LOG2 : 0; }
+int resident_clusters(int num_sms, int size);
 
 // M x N outputs (N: channels of GLU) over a contraction of kb stages: the cut
 // with the least time by these rates (us; measured, see the header):
@@ -982,7 +1036,9 @@ int part_rows_log2(int64_t M) { return M > 1 << PART_ROWS_LOG2 ? PART_ROWS_LOG2 
 //             and its bytes into one SM (full waves of pairs, several row units:
 //             0.29 us at 64 columns, 0.32 at 128, 0.35 from 160 to 256)
 //   all       the weights from HBM
-//   a split, a share   the partial sums written and read back, and the join's launch
+//   a split, a share   the partial sums written and read back, and the join's
+//             launch; in a cluster the exchange, and its clusters must all be
+//             resident (a second wave took one row of d 1544, f 5656 from 24 to 32 us)
 // Dealt stages are taken where they save a twentieth.  Not for one row unit,
 // whose time is the weights' (256 rows, d 2560, f 10240: 55 us, with them 57),
 // nor behind four waves (16384 rows 1666 us, with them 1706).
@@ -995,6 +1051,8 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
     const int step = bmn ? (pair ? 128 : 64) : (pair ? 32 : 16);
     const int a_rows = !pair && !amn ? (int)(M + 7) / 8 * 8 : BM;
     const int64_t m_units = pair ? (M + 2 * BM - 1) / (2 * BM) : 1;
+    int resident[MAX_CLUSTER + 1] = {};
+    for (int k = 2; k <= MAX_CLUSTER && !pair; ++k) resident[k] = resident_clusters(num_sms, k);
     const int keep = pair ? (dglu ? IN_AREA : STAGING) : 0;      // the epilogue's end of the area
     for (int bn = MAX_BN; bn >= (bmn ? step : 64); bn -= step) {
         const int width = glu ? bn / 2 : bn;
@@ -1006,16 +1064,18 @@ Plan search_plan(int num_sms, int64_t M, int64_t N, int kb, bool glu, bool dglu,
         const double bytes = (a_bytes + b_bytes) / 80e3;
         const double stage = std::max(std::max(0.365 * bn / 256, 1.4 / stages),
                                       m_units > 1 ? std::min(0.03 + bytes, 0.355) : bytes);
-        for (int splits = 1; splits <= 16 && splits * 4 <= std::max(kb, 4); ++splits) {
-            if (splits > 1 && tiles * (splits - 1) >= workers) break;
+        for (int splits = 1; splits <= (pair ? 16 : MAX_CLUSTER) && splits * 4 <= std::max(kb, 4); ++splits) {
+            if (splits > 1 && pair && tiles * (splits - 1) >= workers) break;
+            if (splits > 1 && !pair && tiles > resident[splits]) continue;
             const int64_t waves = (tiles * splits + workers - 1) / workers;
             const double units = waves * ((kb + splits - 1) / splits) * stage, hbm = (double)kb * ROWB * cols / 6.4e6;
             double cost = std::max(units, hbm) + 0.2 * std::min(units, hbm);     // they overlap, but not wholly
-            if (splits > 1) cost += 3.0 + (double)splits * M * cols * 8 / 6e6;
+            if (splits > 1)
+                cost += pair ? 3.0 + (double)splits * M * cols * 8 / 6e6 : 0.7 + (double)M * (bn / 15e3 + 1 / 64.0);
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
                 best = Plan{pair, bn, (int)m_units, (int)n_tiles, kb, splits, a_bytes, b_bytes, stages, 0, 0, 0, 0,
-                            splits > 1 ? align256((size_t)splits * part_size(M, (int)cols, part_rows_log2(M)) * 16) : 0};
+                            pair && splits > 1 ? align256((size_t)splits * part_size(M, (int)cols) * 16) : 0};
             }
         }
         // two column tiles at once, in one wave: A is read once for both; both epilogues come behind all MMAs (4 us)
@@ -1078,10 +1138,45 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     return e.plan;
 }
 
-template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, bool MIXED = false, bool DUAL = false>
+// Clusters of `size` CTAs that the current device holds at once, at a CTA an SM
+// (148 SMs in their partitions: 74 of 2, 45 of 3, 33 of 4, 26 of 5, 22 of 6, 15
+// of 7 and of 8); the share of the SMs where it cannot be asked.
+int resident_clusters(int num_sms, int size) {
+    static std::mutex mu;
+    static int known[64][MAX_CLUSTER + 1] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return num_sms * 4 / 5 / size;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[dev][size];
+    if (n == 0) {
+        auto kernel = ffn_kernel<EPI_OUT, false, false, false, false, false, false, CLUSTER>;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms / size * size), 1, 1);
+        cfg.blockDim = dim3(THREADS, 1, 1);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = num_sms * 4 / 5 / size;
+        }
+    }
+    return n;
+}
+
+template <int EPI, bool GLU, bool AMN, bool BMN, bool PAIR, bool F8, bool GELU, int MODE>
 cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnParams& p, int num_sms, bool pdl,
                        cudaStream_t s) {
-    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU, MIXED, DUAL>;
+    auto kernel = ffn_kernel<EPI, GLU, AMN, BMN, PAIR, F8, GELU, MODE>;
+    constexpr bool CL = MODE == CLUSTER;
     static std::mutex mu;
     static int max_units[64] = {};              // CTAs or pairs resident at once, per device
     int dev = 0;
@@ -1094,9 +1189,9 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 0;
-    if (PAIR) {
+    if (PAIR || CL) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.x = CL ? p.splits : 2;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.numAttrs = 1;
@@ -1121,8 +1216,8 @@ cudaError_t launch_one(const CUtensorMap& ma, const CUtensorMap& mb, const FfnPa
     }
     const int64_t units = (int64_t)p.m_units * p.n_tiles * p.splits;
     if (units >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-    // MIXED: every worker that stages are dealt to has to be there, resident at once or not
-    const int64_t grid = MIXED ? std::max<int64_t>(num_sms / 2, p.dealt) : std::min<int64_t>(units, cap);
+    // CLUSTER: a unit each.  MIXED: every worker that stages are dealt to has to be there, resident at once or not
+    const int64_t grid = MODE == MIXED_TAIL ? std::max<int64_t>(num_sms / 2, p.dealt) : CL ? units : std::min<int64_t>(units, cap);
     cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) * grid), 1, 1);
     if (pdl) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1162,7 +1257,6 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     p.shares = pl.shares;
     p.status = c->d_status;
     p.part = part;
-    p.part_rows = part_rows_log2(M);
     p.b_rows = pl.dual ? pl.bn : GLU || pl.pair ? pl.bn / 2 : pl.bn;
     // fp32 accumulator; formats bf16 (or E4M3: 0); MN-major bits; N / 8; M / 16
     p.idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
@@ -1176,21 +1270,25 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     cudaError_t e;
     constexpr bool ACT = EPI == EPI_GLU || EPI == EPI_DGLU;
     const bool gelu = ACT && p.act == ENGRAM_ACT_GELU;
-    if (GLU && pl.dual)
-        e = gelu ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT, false, GLU>(ma, mb, p, c->num_sms, pdl, s)
-                 : launch_one<EPI, GLU, AMN, BMN, true, F8, false, false, GLU>(ma, mb, p, c->num_sms, pdl, s);
+    auto go = [&](auto pair, auto mode) {
+        constexpr bool PAIR = decltype(pair)::value;
+        constexpr int MODE = decltype(mode)::value;
+        constexpr int E = MODE == SPLIT ? EPI_PART : EPI;
+        return gelu && E == EPI ? launch_one<E, GLU, AMN, BMN, PAIR, F8, ACT && E == EPI, MODE>(ma, mb, p, c->num_sms, pdl, s)
+                                : launch_one<E, GLU, AMN, BMN, PAIR, F8, false, MODE>(ma, mb, p, c->num_sms, pdl, s);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (pl.splits > 1)
+        e = pl.pair ? go(Yes{}, std::integral_constant<int, SPLIT>{}) : go(No{}, std::integral_constant<int, CLUSTER>{});
+    else if (!pl.pair)
+        e = go(No{}, std::integral_constant<int, WHOLE>{});
+    else if (GLU && pl.dual)
+        e = go(Yes{}, std::integral_constant<int, GLU ? TWO_TILES : WHOLE>{});
     else if (pl.dealt > 0)
-        e = gelu ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT, true>(ma, mb, p, c->num_sms, pdl, s)
-                 : launch_one<EPI, GLU, AMN, BMN, true, F8, false, true>(ma, mb, p, c->num_sms, pdl, s);
-    else if (pl.splits > 1)
-        e = pl.pair ? launch_one<EPI_PART, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
-                    : launch_one<EPI_PART, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
-    else if (gelu)
-        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8, ACT>(ma, mb, p, c->num_sms, pdl, s)
-                    : launch_one<EPI, GLU, AMN, BMN, false, F8, ACT>(ma, mb, p, c->num_sms, pdl, s);
+        e = go(Yes{}, std::integral_constant<int, MIXED_TAIL>{});
     else
-        e = pl.pair ? launch_one<EPI, GLU, AMN, BMN, true, F8, false>(ma, mb, p, c->num_sms, pdl, s)
-                    : launch_one<EPI, GLU, AMN, BMN, false, F8, false>(ma, mb, p, c->num_sms, pdl, s);
+        e = go(Yes{}, std::integral_constant<int, WHOLE>{});
     prof_end(c, s);
     if (e == cudaSuccess && pl.dealt > 0) {
         prof_begin(c, s, "ffn_join");
@@ -1200,13 +1298,12 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
                  : launch_after(c, ffn_join_mixed_kernel<EPI, F8, false>, blocks, dim3(256), 0, s, p);
         prof_end(c, s);
     }
-    if (e == cudaSuccess && pl.splits > 1) {
+    if (e == cudaSuccess && pl.splits > 1 && pl.pair) {
         prof_begin(c, s, "ffn_join");
-        const int64_t threads = part_size(M, (int)N, p.part_rows) / 2;
+        const int64_t threads = part_size(M, (int)N) / 2;
         const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)c->num_sms * 8);
-        auto join = [&](auto* kernel) { return launch_after(c, kernel, blocks, dim3(256), 0, s, p); };
-        e = p.part_rows ? (gelu ? join(ffn_join_kernel<EPI, ACT, PART_ROWS_LOG2>) : join(ffn_join_kernel<EPI, false, PART_ROWS_LOG2>))
-                        : (gelu ? join(ffn_join_kernel<EPI, ACT, 0>) : join(ffn_join_kernel<EPI, false, 0>));
+        e = gelu ? launch_after(c, ffn_join_kernel<EPI, ACT>, blocks, dim3(256), 0, s, p)
+                 : launch_after(c, ffn_join_kernel<EPI, false>, blocks, dim3(256), 0, s, p);
         prof_end(c, s);
     }
     return e;

@@ -140,6 +140,20 @@ def test_ffn_shared_tiles(eb, n, d, f, kind):
     test_ffn_grad(eb, n, d, f, kind)
 
 
+# Few rows: the CTAs that split a tile's contraction add their sums through each other's shared memory.
+@pytest.mark.parametrize("n,d,f", [(1, 1152, 1456), (4, 1280, 1488), (37, 1784, 1960), (100, 1024, 4096), (128, 136, 5000)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_ffn_few_rows(eb, n, d, f, kind):
+    test_ffn(eb, n, d, f, kind, kind == "gelu")
+    test_ffn_grad(eb, n, d, f, kind)
+
+
+@pytest.mark.parametrize("n,d,f", [(1, 2560, 512), (3, 384, 1952), (20, 384, 7824), (128, 2432, 312)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_ffn_few_rows_fp8(eb, n, d, f, kind):
+    test_ffn_fp8(eb, n, d, f, kind)
+
+
 # Between one and two waves of gate and up tiles: a pair takes two at once; the last pair of an odd number has one.
 @pytest.mark.parametrize("n,d,f", [(200, 2560, 10240), (512, 2560, 5000), (700, 2048, 4096)])
 @pytest.mark.parametrize("kind,with_res", [("silu", True), ("gelu", False)])
