@@ -525,8 +525,8 @@ ENGRAM_API engram_status engram_add_norm_grad(engram_ctx* ctx, const void* d_y, 
  *   res  [n][d] bf16 or null, added in fp32 before y's one rounding;
  *   y    [n][d] bf16; may be res or x;
  *   saved  null, or engram_ffn_saved_bytes(ctx, n, f) bytes for the
- *        backward (bf16 contexts): act(g) * u in bf16, and g and u with 24 of
- *        their 32 bits.
+ *        backward (bf16 contexts): act(g) * u in bf16, and g and u rounded to
+ *        24 of their 32 bits (2^-16 of a value at most).
  * f is a multiple of 8, all tensors 16-byte aligned.  Scratch:
  * engram_ffn_workspace_bytes(ctx, n, f) bytes, 256-byte aligned.
  *
