@@ -19,7 +19,7 @@ from .binding import (  # noqa: F401  (re-exported C ABI names)
     ENGRAM_NOALLOC_SCRATCH_BYTES, engram_destroy, engram_device_status, engram_forward, engram_forward_noalloc,
     engram_forward_host, engram_gate_conv, engram_gather, engram_gather_staged, engram_hash, engram_host_dedupe,
     engram_host_fetch, engram_host_tier_create, engram_host_tier_destroy, engram_host_tier_stats,
-    engram_host_workspace_bytes, engram_pack_rows, engram_debug_stall_next, engram_host_tier_debug,
+    engram_host_workspace_bytes, engram_pack_rows, engram_debug_stall_next, engram_debug_ffn_cut, engram_host_tier_debug,
     ENGRAM_INJECT_LIST_WAIT, ENGRAM_INJECT_PACK_ABANDON, engram_host_cache_enable, engram_host_cache_reset,
     engram_host_cache_stats, engram_shard_range, engram_forward_sharded, engram_ipc_export, engram_ipc_open,
     engram_ipc_close, ENGRAM_IPC_HANDLE_BYTES, ENGRAM_MAX_SHARDS, engram_multibranch_workspace_bytes,

@@ -46,7 +46,7 @@ EXPORTS = ("engram_create", "engram_destroy", "engram_strerror", "engram_last_er
            "engram_grad_route", "engram_grad_combine_workspace_bytes", "engram_grad_combine", "engram_shard_sgd",
            "engram_embed", "engram_embed_grad_workspace_bytes", "engram_embed_grad", "engram_add_norm",
            "engram_add_norm_grad_workspace_bytes", "engram_add_norm_grad", "engram_ffn_workspace_bytes", "engram_ffn",
-           "engram_ffn_saved_bytes", "engram_ffn_grad_workspace_bytes", "engram_ffn_grad")
+           "engram_ffn_saved_bytes", "engram_ffn_grad_workspace_bytes", "engram_ffn_grad", "engram_debug_ffn_cut")
 ENGRAM_ACT_SILU, ENGRAM_ACT_GELU = 0, 1
 ENGRAM_MAX_BRANCHES = 4
 ENGRAM_IPC_HANDLE_BYTES = 64
@@ -110,6 +110,7 @@ _sigs = {
     "engram_host_tier_stats": ([_vp, ctypes.c_void_p], _st),
     "engram_pack_rows": ([_vp, _i64, _sz, _vp, _i64, _vp, _i32], _st),
     "engram_debug_stall_next": ([_vp], _st),
+    "engram_debug_ffn_cut": ([_vp, _i64, _i32, _i32], _i32),
     "engram_host_tier_debug": ([_vp, ctypes.c_uint32, ctypes.c_double], _st),
     "engram_host_cache_enable": ([_vp, _i64, _i32], _st),
     "engram_host_tier_map": ([_vp], _st),
@@ -531,6 +532,12 @@ def engram_pack_rows(host_tables, total_rows: int, row_bytes: int, rows, n: int,
         return x.ctypes.data if hasattr(x, "ctypes") else x.data_ptr()
     _check(_lib.engram_pack_rows(addr(host_tables), total_rows, row_bytes, addr(rows), n, addr(dst), n_threads),
            "engram_pack_rows")
+
+
+def engram_debug_ffn_cut(ctx, n: int, f: int, product: int):
+    """Test hook: (form, on CTA pairs) of a feed-forward product's cut, None for arguments the call refuses."""
+    cut = int(_lib.engram_debug_ffn_cut(ctx, n, f, product))
+    return None if cut < 0 else (("whole", "split", "dealt", "two tiles", "cluster")[cut >> 1], bool(cut & 1))
 
 
 def engram_debug_stall_next(ctx) -> None:

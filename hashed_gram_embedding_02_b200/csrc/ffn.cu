@@ -1145,6 +1145,12 @@ Plan make_plan(const engram_ctx* c, int64_t M, int64_t N, int kb, bool glu, bool
     return e.plan;
 }
 
+// the kernel form that a cut takes
+int form_of(const Plan& pl) {
+    if (pl.splits > 1) return pl.pair ? SPLIT : CLUSTER;
+    return pl.dual ? TWO_TILES : pl.dealt > 0 ? MIXED_TAIL : WHOLE;
+}
+
 // Clusters of `size` CTAs that the current device holds at once, at a CTA an SM
 // (148 SMs in their partitions: 74 of 2, 45 of 3, 33 of 4, 26 of 5, 22 of 6, 15
 // of 7 and of 8); the share of the SMs where it cannot be asked.
@@ -1286,16 +1292,13 @@ cudaError_t product(engram_ctx* c, const void* A, int64_t lda, const void* B, in
     };
     using Yes = std::true_type;
     using No = std::false_type;
-    if (pl.splits > 1)
-        e = pl.pair ? go(Yes{}, std::integral_constant<int, SPLIT>{}) : go(No{}, std::integral_constant<int, CLUSTER>{});
-    else if (!pl.pair)
-        e = go(No{}, std::integral_constant<int, WHOLE>{});
-    else if (GLU && pl.dual)
-        e = go(Yes{}, std::integral_constant<int, GLU ? TWO_TILES : WHOLE>{});
-    else if (pl.dealt > 0)
-        e = go(Yes{}, std::integral_constant<int, MIXED_TAIL>{});
-    else
-        e = go(Yes{}, std::integral_constant<int, WHOLE>{});
+    switch (form_of(pl)) {
+        case SPLIT: e = go(Yes{}, std::integral_constant<int, SPLIT>{}); break;
+        case CLUSTER: e = go(No{}, std::integral_constant<int, CLUSTER>{}); break;
+        case TWO_TILES: e = go(Yes{}, std::integral_constant<int, GLU ? TWO_TILES : WHOLE>{}); break;
+        case MIXED_TAIL: e = go(Yes{}, std::integral_constant<int, MIXED_TAIL>{}); break;
+        default: e = pl.pair ? go(Yes{}, std::integral_constant<int, WHOLE>{}) : go(No{}, std::integral_constant<int, WHOLE>{});
+    }
     prof_end(c, s);
     if (e == cudaSuccess && pl.dealt > 0) {
         prof_begin(c, s, "ffn_join");
@@ -1341,20 +1344,27 @@ struct FfnWs {
     size_t bytes;
 };
 
-FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad) {
+// The products of a call, in the order that engram_debug_ffn_cut numbers them.
+enum { GATE_UP, DOWN, D_GATE_UP, D_WD, D_X, D_WGU, PRODUCTS };
+
+Plan plan_of(const engram_ctx* c, int64_t n, int64_t f, int product) {
     const int64_t d = c->cfg.hidden;
-    auto kb = [](int64_t K) { return (int)((K + 63) / 64); };
-    size_t part = 0;
-    if (grad) {
-        part = std::max(part, make_plan(c, n, f, kb(d), false, true, false, true).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(2 * f), false, false, false, true).part_bytes);
-        part = std::max(part, make_plan(c, d, f, kb(n), false, false, true, true).part_bytes);
-        part = std::max(part, make_plan(c, 2 * f, d, kb(n), false, false, true, true).part_bytes);
-    } else {
-        const bool f8 = c->cfg.dtype == ENGRAM_FP8;
-        part = std::max(part, make_plan(c, n, f, (int)((d + (f8 ? 127 : 63)) / (f8 ? 128 : 64)), true, false, false, false).part_bytes);
-        part = std::max(part, make_plan(c, n, d, kb(f), false, false, false, false).part_bytes);
+    const int k8 = c->cfg.dtype == ENGRAM_FP8 && product == GATE_UP ? 128 : 64;
+    auto kb = [&](int64_t K) { return (int)((K + k8 - 1) / k8); };
+    switch (product) {
+        case GATE_UP: return make_plan(c, n, f, kb(d), true, false, false, false);
+        case DOWN: return make_plan(c, n, d, kb(f), false, false, false, false);
+        case D_GATE_UP: return make_plan(c, n, f, kb(d), false, true, false, true);
+        case D_WD: return make_plan(c, d, f, kb(n), false, false, true, true);
+        case D_X: return make_plan(c, n, d, kb(2 * f), false, false, false, true);
+        default: return make_plan(c, 2 * f, d, kb(n), false, false, true, true);
     }
+}
+
+FfnWs ffn_carve(const engram_ctx* c, void* base, int64_t n, int64_t f, bool grad) {
+    size_t part = 0;
+    for (int k = grad ? D_GATE_UP : GATE_UP; k < (grad ? PRODUCTS : D_GATE_UP); ++k)
+        part = std::max(part, plan_of(c, n, f, k).part_bytes);
     FfnWs w{};
     char* p = static_cast<char*>(base);
     auto take = [&](size_t bytes) {
@@ -1402,6 +1412,14 @@ engram_status check_ws(const void* workspace, size_t have, size_t need) {
 using namespace engram;
 
 extern "C" {
+
+int32_t engram_debug_ffn_cut(const engram_ctx* c, int64_t n, int32_t f, int32_t product) {
+    if (product < 0 || product >= PRODUCTS || n < 1 ||
+        ffn_shape(c, n, f, ENGRAM_ACT_SILU, product >= D_GATE_UP) != ENGRAM_OK)
+        return -1;
+    const Plan pl = plan_of(c, n, f, product);
+    return form_of(pl) * 2 + (pl.pair ? 1 : 0);
+}
 
 size_t engram_ffn_workspace_bytes(const engram_ctx* c, int64_t n, int32_t f) {
     if (ffn_shape(c, n, f, ENGRAM_ACT_SILU, false) != ENGRAM_OK) return 0;

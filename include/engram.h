@@ -166,6 +166,14 @@ ENGRAM_API int32_t engram_profile_read(engram_ctx* ctx, float* ms, const char** 
  * next call.  The outputs of the stalled call are undefined.  One shot. */
 ENGRAM_API engram_status engram_debug_stall_next(engram_ctx* ctx);
 
+/* Test hook: how a product of a feed-forward call of n rows and inner width f
+ * is cut on this context's device, so that a test can ask for the kernel form
+ * it means to run.  product: 0 gate/up, 1 down, 2 d_gate_up, 3 d_Wd, 4 d_x,
+ * 5 d_Wgu.  Returns 2 * form + (1 on CTA pairs), form 0 whole tiles, 1 split
+ * contraction with partial sums, 2 dealt tail, 3 two tiles at once, 4 split
+ * contraction in a cluster; -1 for arguments that the call refuses. */
+ENGRAM_API int32_t engram_debug_ffn_cut(const engram_ctx* ctx, int64_t n, int32_t f, int32_t product);
+
 /* Synchronise `stream`, return the device status word in *flags (nullable)
  * and clear it.  ENGRAM_OK when it was zero, ENGRAM_E_TIMEOUT when the
  * timeout bit was set, else ENGRAM_E_DEVICE. */
