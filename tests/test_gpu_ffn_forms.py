@@ -19,7 +19,7 @@ function):
 
 import pytest
 
-from test_gpu_ffn import test_ffn_grad as check_grad
+from test_gpu_ffn import test_ffn_fp8 as check_fp8, test_ffn_grad as check_grad
 from test_gpu_residual import engine
 
 torch = pytest.importorskip("torch")
@@ -66,3 +66,20 @@ def test_weight_gradients_in_a_cluster(eb, n, d, f, in_cluster, kind):
     for name in in_cluster:
         assert cut(eb, eng, n, f, name) == ("cluster", False), name
     check_grad(eb, n, d, f, kind)
+
+
+# E4M3 operands, tiles that do not fill a wave of SM pairs: the shares are raw sums, and the join applies the scales.
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d,f", [(1095, 3200, 3728), (552, 3200, 6392), (3777, 3584, 1280)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_dealt_tail_fp8(eb, n, d, f, kind):
+    assert cut(eb, engine(eb, d, dtype="fp8"), n, f, "gate_up") == ("dealt", True)
+    check_fp8(eb, n, d, f, kind)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d,f", [(6389, 2560, 296), (300, 4096, 6000)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_two_tiles_fp8(eb, n, d, f, kind):
+    assert cut(eb, engine(eb, d, dtype="fp8"), n, f, "gate_up") == ("two tiles", True)
+    check_fp8(eb, n, d, f, kind)
