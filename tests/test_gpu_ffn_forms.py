@@ -17,9 +17,11 @@ function):
   with a relative error D before it is within m / (1 + m) + (1 + m) D, which is
   at most m + 2^-17 as long as D <= (2^-17 + m^2 / (1 + m)) / (1 + m) = 2.27e-5."""
 
+import time
+
 import pytest
 
-from test_gpu_ffn import test_ffn_fp8 as check_fp8, test_ffn_grad as check_grad
+from test_gpu_ffn import inputs, test_ffn_fp8 as check_fp8, test_ffn_grad as check_grad
 from test_gpu_residual import engine
 
 torch = pytest.importorskip("torch")
@@ -83,3 +85,29 @@ def test_dealt_tail_fp8(eb, n, d, f, kind):
 def test_two_tiles_fp8(eb, n, d, f, kind):
     assert cut(eb, engine(eb, d, dtype="fp8"), n, f, "gate_up") == ("two tiles", True)
     check_fp8(eb, n, d, f, kind)
+
+
+# A stage that is announced and never loaded, in each form of the gate/up product: the waits run out, CTAs that did not
+# abort meet those that did at their barriers, the joins add sums that were never written, and the down product, which
+# may have started early, gives up too.  All of it ends by itself, and the next call gives the right bits.
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d,f,form", [(1, 1152, 1456, ("cluster", False)), (512, 2560, 5000, ("two tiles", True)),
+                                        (300, 2560, 264, ("split", True)), (6389, 2504, 296, ("dealt", True))])
+@pytest.mark.parametrize("save", [False, True])
+def test_stalled_forms_time_out_and_the_context_recovers(eb, n, d, f, form, save):
+    eng = engine(eb, d)
+    assert cut(eb, eng, n, f, "gate_up") == form
+    x, Wgu, Wd = inputs(n, d, f)
+    want = eng.ffn(x, Wgu, Wd, save=True)
+    torch.cuda.synchronize()
+    eb.engram_debug_stall_next(eng.ctx)
+    t0 = time.time()
+    eng.ffn(x, Wgu, Wd, save=save)
+    st, flags = eng.status()
+    assert st == eb.ENGRAM_E_TIMEOUT and flags & eb.ENGRAM_ERR_TIMEOUT, (st, flags)
+    assert time.time() - t0 < 30.0
+    again = eng.ffn(x, Wgu, Wd, save=True)
+    assert torch.equal(again[0], want[0])
+    a = n * ((f + 63) // 64 * 64) * 2                     # the saved a: its rows' padding is not written
+    assert torch.equal(again[1][:a].view(n, -1)[:, :f * 2], want[1][:a].view(n, -1)[:, :f * 2])
+    assert eng.status() == (eb.ENGRAM_OK, 0)
