@@ -67,3 +67,68 @@ def test_ffn_gradients_beyond_32_bit_offsets(eb, few):
     assert float(d_Wgu.max()) < 2 ** 24 and float(d_Wd.max()) < 2 ** 24
     assert torch.equal(got[1], d_Wgu.float().to(bf))
     assert torch.equal(got[2], d_Wd.float().to(bf))
+
+
+def runs(B, T, V, lengths, seed):
+    """tokens of B x T positions: token 2 k + 1 occurs lengths[k] times, the rest of the batch is spread over the even
+    tokens below V / 2 (the runs lie among them in the sorted list), all in random order"""
+    rng = np.random.default_rng(seed)
+    long = np.concatenate([np.full(m, 2 * k + 1) for k, m in enumerate(lengths)])
+    rest = 2 * rng.integers(0, V // 4, B * T - long.size)
+    t = np.concatenate([long, rest])
+    return torch.from_numpy(rng.permutation(t).reshape(B, T).astype(np.int32)).cuda()
+
+
+# Runs from one position to half of the batch, at lengths around the pieces (8 or 32 sorted entries) and around the
+# counts where the join's groups (256 / lanes of them, lanes = the power of two from d / 4 up, 64 at most) take one part
+# more each.
+LENGTHS = [1, 2, 7, 8, 9, 31, 32, 33, 63, 64, 65, 100, 128, 250, 500, 1023, 1024, 1025, 3999, 4000, 4095, 4097, 4128]
+
+
+def summation_depth(count, d, piece):
+    """Additions in a row that a term of a run can pass through: in its piece, in its group of the join, over the
+    groups, and the product with the scale.  embed_reduce_kernel adds at most `piece` terms; the run's m parts lie in
+    ceil(count / piece) pieces or one more; each of the join's groups adds per = ceil(m / groups) of them, and the
+    ceil(m / per) sums are added one after the other."""
+    lanes = 1
+    while lanes < 64 and lanes * 4 < d:
+        lanes *= 2
+    groups = 256 // lanes
+
+    def join(m):
+        per = (m + groups - 1) // groups
+        return per + (m + per - 1) // per
+
+    m = (count + piece - 1) // piece
+    return count.clamp(max=piece) + torch.maximum(join(m), join(m + 1)) + 1
+
+
+@pytest.mark.parametrize("B,T,V,d", [(1, 18000, 4000, 8), (3, 400001, 300000, 8), (2, 30011, 5000, 72), (1, 120007, 5000, 264)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_embed_grad_of_long_runs(eb, B, T, V, d, dtype):
+    eng = engine(eb, d, V, dtype)
+    n = B * T
+    lengths = [m for m in LENGTHS if m <= n // 10]
+    if n > 10 ** 6:
+        lengths.append(n // 2)                            # a token that takes half of the batch
+    tok = runs(B, T, V, lengths, 5)
+    idx = tok.view(-1).long()
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(6)
+
+    def plain(t):
+        return torch.zeros(V, d, dtype=torch.float64, device="cuda").index_add_(0, idx, t.double())
+
+    whole = torch.randint(-3, 4, (n, d), generator=gen, device="cuda").to(dt)
+    assert torch.equal(eng.embed_grad(tok, whole), plain(whole).float())       # exact: below 2^24
+    was = torch.randint(-9, 10, (V, d), generator=gen, device="cuda").float()
+    got = eng.embed_grad(tok, whole, out=was.clone(), accumulate=True)
+    assert torch.equal(got, (plain(whole) + was.double()).float())
+    # positive terms: nothing cancels, so that the bound is a relative one
+    t = (0.5 + torch.rand(n, d, generator=gen, device="cuda")).to(dt)
+    want, count = plain(t), torch.bincount(idx, minlength=V)[:, None]
+    piece = 32 if n >= 32 * 4 * torch.cuda.get_device_properties(0).multi_processor_count else 8
+    bound = summation_depth(count.clamp(min=1), d, piece) * 2.0 ** -24 * want
+    got = eng.embed_grad(tok, t)
+    assert bool(((got.double() - want).abs() <= bound).all())
+    assert torch.equal(got, eng.embed_grad(tok, t))
