@@ -23,8 +23,9 @@
 //   3. join: the parts of each cut run, in order.
 // Between 1 and 2 the rows of the tokens that do not occur are cleared (a small
 // dE is cleared whole by the sort's first launch).
-// The order of every sum depends on the tokens alone.  The launches behind the
-// first are programmatic dependents of one another: each waits at its start
+// The order of a token's sum is fixed by its positions and by where its run lies
+// among the pieces, whose length depends on the row count and the SMs (piece_of).
+// The launches behind the first are programmatic dependents of one another: each waits at its start
 // for the one before, which hides most of its launch.
 #include <algorithm>
 

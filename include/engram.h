@@ -476,8 +476,9 @@ ENGRAM_API engram_status engram_shard_sgd(engram_ctx* ctx, int32_t n_shards, int
  * dtype.  accumulate = 0 writes every row of d_E (zero where v does not
  * occur); otherwise the rows of the tokens that occur are added to and no
  * other row is touched.  The tokens are sorted and the sums run in fp32 in an
- * order that depends on the tokens alone, so the result is the same on every
- * run.  Rows with an id outside [0, V) contribute nothing and set
+ * order fixed by the tokens, the row count and the device (its SM count), so
+ * the result is the same on every run.  Rows with an id outside [0, V)
+ * contribute nothing and set
  * ENGRAM_ERR_TOKEN.  At most 2^24 rows.  Scratch:
  * engram_embed_grad_workspace_bytes(ctx, B*L) bytes, 256-byte aligned (0 when
  * the row count is out of range). */

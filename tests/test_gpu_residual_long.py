@@ -132,3 +132,24 @@ def test_embed_grad_of_long_runs(eb, B, T, V, d, dtype):
     got = eng.embed_grad(tok, t)
     assert bool(((got.double() - want).abs() <= bound).all())
     assert torch.equal(got, eng.embed_grad(tok, t))
+
+
+@pytest.mark.parametrize("T", [300, 2500, 9000, 40000])   # the sorts of one CTA, of several; pieces of 8 and of 32
+def test_embed_grad_row_depends_on_its_own_positions(eb, T):
+    """A token's sum has the same bits whatever the other tokens and rows are, as long as its positions and the number
+    of smaller tokens in the batch (where its run lies among the cuts of the sorted list) stay."""
+    V, v, d = 5000, 2500, 136
+    eng = engine(eb, d, V)
+    rng = np.random.default_rng(T)
+    kind = rng.choice(3, 2 * T, p=[0.3, 0.4, 0.3])        # below v, v itself, above v
+    d_h = torch.randn(2 * T, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    mine = torch.from_numpy(kind == 1).cuda()[:, None]
+    want = None
+    for seed in range(3):
+        other = np.random.default_rng(seed)
+        t = np.where(kind == 0, other.integers(0, v, 2 * T), np.where(kind == 1, v, other.integers(v + 1, V, 2 * T)))
+        rows = torch.where(mine, d_h, torch.full_like(d_h, float("nan") if seed == 2 else seed))
+        got = eng.embed_grad(torch.from_numpy(t.reshape(2, T).astype(np.int32)).cuda(), rows)[v]
+        assert want is None or torch.equal(got, want), seed
+        want = got
+    assert bool(want.isfinite().all())
