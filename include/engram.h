@@ -161,7 +161,8 @@ ENGRAM_API int32_t engram_profile_read(engram_ctx* ctx, float* ms, const char** 
  * MMA warp's wait on that stage runs out after about 2 s.  The kernel then
  * sets ENGRAM_ERR_TIMEOUT, raises its abort flag, drains the copies and MMAs
  * it issued (bounded again), frees its tensor memory and returns; the
- * following kernels run to completion.  engram_device_status then reports
+ * following kernels end too (one that has started early and waits for the
+ * stalled one gives up in the same way).  engram_device_status then reports
  * ENGRAM_E_TIMEOUT, and the context and its workspace stay usable for the
  * next call.  The outputs of the stalled call are undefined.  One shot. */
 ENGRAM_API engram_status engram_debug_stall_next(engram_ctx* ctx);
